@@ -84,11 +84,16 @@ typedef enum pa_dtype {
     PA_DTYPE_FP8_E4M3 = 1
 } pa_dtype;
 
+/* Most drafted tokens a sequence may hold in one pa_decode_tree call (the
+ * bits of a row's mask). */
+#define PA_MAX_TREE_ROWS 64
+
 /* Bits of the device status word (pa_get_last_device_error). */
 #define PA_DEVERR_BAD_BLOCK 0x1u  /* a block-table entry outside [0, num_blocks) was needed */
 #define PA_DEVERR_BAD_SLOT 0x2u   /* a slot mapped past the last block */
-#define PA_DEVERR_BAD_LEN 0x4u    /* seq_len < 0 or > 16 * max_blocks_per_seq (cascade: < 16 * prefix_blocks) */
-#define PA_DEVERR_BAD_PAIR 0x8u   /* a copy pair outside [0, num_blocks) */
+#define PA_DEVERR_BAD_LEN 0x4u    /* seq_len < 0 or > 16 * max_blocks_per_seq (cascade: < 16 * prefix_blocks);
+                                   * tree: a row range or draft count out of bounds; compact: a list past its bounds */
+#define PA_DEVERR_BAD_PAIR 0x8u   /* a copy pair outside [0, num_blocks); compact: a list that does not ascend */
 #define PA_DEVERR_TIMEOUT 0x10u   /* a bounded wait for an async copy or MMA gave up (results invalid) */
 #define PA_DEVERR_LAYOUT 0x20u    /* prefill: the CTA's shared memory did not start on a 1 KB boundary (no output written) */
 
@@ -314,6 +319,127 @@ int pa_decode_noalloc(void *out, const void *q, const void *k_cache, const void 
                       pa_stream_t stream);
 
 /*
+ * The four calls below have no counterpart in the source pages: they serve
+ * speculative decoding (several drafted tokens verified in one step) and
+ * caches held to a budget, over the same cache and block tables.
+ *
+ * pa_decode_tree -- attention of drafted tokens, arranged in a tree, over
+ * the sequence's cached prefix and over the drafts each one may see.
+ *
+ *   out, q        bf16 [total_q][num_q_heads][head_dim].
+ *   cu_q_lens     int32 [num_seqs+1]: sequence b owns rows
+ *                 cu_q_lens[b]..cu_q_lens[b+1]-1, its drafts, at most
+ *                 max_q_len of them (0 is allowed).
+ *   prefix_lens   int32 [num_seqs]: tokens in the cache before the drafts;
+ *                 draft j of sequence b lies at position prefix_lens[b] + j
+ *                 of its block table (written there first, pa_write_kv).
+ *   mask          uint64 [total_q]: a row attends the whole prefix and draft
+ *                 j of its sequence for every set bit j (its own bit
+ *                 included: a token tree sets the bits of the ancestors and
+ *                 the token itself).  Bits past the sequence's last draft
+ *                 are ignored.  A row that may see nothing (no prefix, no
+ *                 bit) gets zeros.
+ *   block_tables  int32 [num_seqs][max_blocks_per_seq].
+ *   max_q_len     host upper bound on any sequence's drafts, in
+ *                 [0, PA_MAX_TREE_ROWS].
+ *   total_q_tokens  rows of q and out, at most num_seqs * max_q_len.  Rows
+ *                 behind cu_q_lens[num_seqs] are left as they are.
+ *   scale         softmax scale, positive and finite (else
+ *                 PA_ERR_INVALID_ARG).
+ *   k_scale, v_scale  fp32 [num_kv_heads] for an fp8 cache, else ignored.
+ *   workspace     device scratch of at least pa_decode_tree_workspace_size()
+ *                 bytes, 256-byte aligned, no initialisation needed.  Calls
+ *                 that share one must not overlap on the GPU.
+ * A sequence whose lengths are out of range (more drafts than max_q_len,
+ * rows past total_q_tokens, prefix + drafts past the block table) is flagged
+ * PA_DEVERR_BAD_LEN and its rows are left as they are.  num_seqs in
+ * [0, 2048]; num_kv_heads <= 128; num_q_heads / num_kv_heads in {1,2,4,8};
+ * head_dim 64 or 128; bf16 or fp8 E4M3 cache.  fp32 accumulation, rounded to
+ * bf16 once at the end.
+ */
+int pa_decode_tree_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_q_len,
+                                  int32_t max_blocks_per_seq, const pa_cache_desc *desc, size_t *bytes);
+
+int pa_decode_tree(void *out, const void *q, const int32_t *cu_q_lens, const int32_t *prefix_lens,
+                   const uint64_t *mask, const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                   int32_t num_q_heads, int32_t max_q_len, int32_t total_q_tokens, const void *k_cache,
+                   const void *v_cache, float scale, const float *k_scale, const float *v_scale, void *workspace,
+                   size_t workspace_bytes, const pa_cache_desc *desc, pa_stream_t stream);
+
+/*
+ * pa_decode_weights -- pa_decode, and every cached token's attention weight
+ * added to a running sum kept beside the cache:
+ *     weights[blk][k][t%16] = (t < seen_lens[b] ? weights[blk][k][t%16] : 0)
+ *                             + sum_{h in group k} softmax_t(scale q[b][h] . k_t)
+ * for every token t < seq_lens[b], blk = block_tables[b][t/16], kv head k.
+ *
+ *   weights       fp32 [num_blocks][num_kv_heads][16], 16-byte aligned;
+ *                 slots of no cached token are left as they are.
+ *   seen_lens     int32 [num_seqs] or NULL: positions whose sum is there
+ *                 already; the others start at zero, so a slot needs no
+ *                 clearing when its block is handed out.  NULL adds to all.
+ *   out, q, caches, block_tables, seq_lens, scale, scales, limits as
+ *                 pa_decode (balanced split).
+ *   workspace     at least pa_decode_weights_workspace_size() bytes, 256-byte
+ *                 aligned, no initialisation needed; not shared by calls that
+ *                 overlap on the GPU.
+ * Sequences of one call must hold distinct blocks: a slot that two of them
+ * reach (a shared prompt) gets an unspecified one of the two sums.
+ */
+int pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                     const pa_cache_desc *desc, size_t *bytes);
+
+int pa_decode_weights(void *out, float *weights, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *block_tables, const int32_t *seq_lens, const int32_t *seen_lens,
+                      int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_q_heads, float scale,
+                      const float *k_scale, const float *v_scale, void *workspace, size_t workspace_bytes,
+                      const pa_cache_desc *desc, pa_stream_t stream);
+
+/*
+ * pa_select_tokens -- which cached tokens each kv head keeps under a budget:
+ * the first num_sink, the last num_recent and, of the rest, the heaviest by
+ * `weights` (pa_decode_weights).  Ties go to the lowest position; NaN counts
+ * as the largest weight, -0 equals +0.
+ *
+ *   keep          int32 [num_seqs][num_kv_heads][budget]: kept positions,
+ *                 ascending, then -1.
+ *   keep_lens     int32 [num_seqs]: min(seq_len, budget), for every head.
+ *   weights       fp32 [num_blocks][num_kv_heads][16], 16-byte aligned.
+ *   block_tables, seq_lens  as pa_decode.  A sequence no longer than the
+ *                 budget keeps every token.
+ * budget >= 1, num_sink + num_recent <= budget, num_seqs in [0, 2048],
+ * num_kv_heads <= 128.  Blocks of a bad table entry count as weight -inf.
+ * Only num_blocks and num_kv_heads of `desc` matter.
+ */
+int pa_select_tokens(int32_t *keep, int32_t *keep_lens, const float *weights, const int32_t *block_tables,
+                     const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t budget,
+                     int32_t num_sink, int32_t num_recent, const pa_cache_desc *desc, pa_stream_t stream);
+
+/*
+ * pa_compact_kv -- move kept tokens together inside the cache, in place: K
+ * and V (and, if given, the weight) of position keep[b][k][i] go to position
+ * start_lens[b] + i, for i < keep_lens[b], kv head k.  After a selection
+ * start is 0 (NULL); after a verification it is the prefix length and the
+ * list is the accepted path's positions.
+ *
+ *   weights       fp32 [num_blocks][num_kv_heads][16] or NULL.
+ *   keep          int32 [num_seqs][keep_heads][max_keep]; keep_heads is
+ *                 num_kv_heads, or 1 for one list that serves every head.
+ *   keep_lens     int32 [num_seqs], each in [0, max_keep].
+ *   start_lens    int32 [num_seqs] or NULL (0).
+ * A list ascends strictly and keep[i] >= start + i; an entry that breaks
+ * this is flagged PA_DEVERR_BAD_PAIR and not moved (the entries after it
+ * still are).  A list or destination past its bounds is flagged
+ * PA_DEVERR_BAD_LEN and its sequence left as it is.  Positions behind the
+ * last kept one keep their old contents.  The blocks moved within must
+ * belong to one sequence of the call only (copy shared ones first,
+ * pa_copy_blocks).
+ */
+int pa_compact_kv(void *k_cache, void *v_cache, float *weights, const int32_t *block_tables, const int32_t *keep,
+                  const int32_t *keep_lens, const int32_t *start_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
+                  int32_t keep_heads, int32_t max_keep, const pa_cache_desc *desc, pa_stream_t stream);
+
+/*
  * pa_get_last_device_error -- synchronise `stream`, return the device status
  * word (PA_DEVERR_* bits, 0 if clean) in *flags and clear it.  Returns
  * PA_ERR_DEVICE if any bit was set, PA_OK otherwise.
@@ -323,8 +449,9 @@ int pa_get_last_device_error(uint32_t *flags, pa_stream_t stream);
 /* Human-readable name of a pa_status value (static string). */
 const char *pa_status_string(int status);
 
-/* Library version as an integer (major*10000 + minor*100 + patch): 300 =
- * 0.3.0, which adds chunked prefill over an fp8 cache and the
+/* Library version as an integer (major*10000 + minor*100 + patch): 400 =
+ * 0.4.0, which adds pa_decode_tree, pa_decode_weights, pa_select_tokens and
+ * pa_compact_kv to 0.3.0; 0.3.0 added chunked prefill over an fp8 cache and the
  * PA_MAX_BLOCKS_PER_SEQ bound to 0.2.0 (pa_decode_cascade,
  * pa_decode_noalloc). */
 int pa_version(void);

@@ -2,6 +2,7 @@
 // validation on the host, then one or two kernel launches on the caller's
 // stream.  No allocation, no synchronisation (except the explicit status
 // query).
+#include <cfloat>
 #include <mutex>
 
 #include "common.cuh"
@@ -56,6 +57,20 @@ int resolve_partition(int32_t partition_tokens, int *out) {
     return PA_OK;
 }
 
+// Checks shared by the calls that attend with GQA groups over block tables.
+int check_attend(const pa_cache_desc *d, int32_t num_seqs, int32_t max_blocks, int32_t num_q_heads) {
+    if (num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks <= 0 || max_blocks > pa::kMaxBlocksPerSeq ||
+        num_q_heads <= 0 || num_q_heads % d->num_kv_heads != 0)
+        return PA_ERR_INVALID_ARG;
+    if (d->num_kv_heads > pa::kMaxDecodeKvHeads) return PA_ERR_UNSUPPORTED;
+    const int G = num_q_heads / d->num_kv_heads;
+    return G == 1 || G == 2 || G == 4 || G == 8 ? PA_OK : PA_ERR_UNSUPPORTED;
+}
+
+bool bad_workspace(const void *ws, size_t have, size_t need) {
+    return need > 0 && (!ws || have < need || (reinterpret_cast<uintptr_t>(ws) & 255));
+}
+
 }  // namespace
 
 unsigned *pa::status_word() { return status_word_ptr(); }
@@ -72,7 +87,7 @@ int pa::sm_count() {
 
 extern "C" {
 
-int pa_version(void) { return 300; }
+int pa_version(void) { return 400; }
 
 const char *pa_status_string(int status) {
     switch (status) {
@@ -235,6 +250,114 @@ int pa_prefill_chunk(void *out, const void *q, const int32_t *cu_q_lens, const i
         a.v_scale = v_scale;
     }
     return from_cuda(pa::launch_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_decode_tree_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_q_len,
+                                  int32_t max_blocks_per_seq, const pa_cache_desc *desc, size_t *bytes) {
+    int rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    rc = check_attend(desc, num_seqs, max_blocks_per_seq, num_q_heads);
+    if (rc != PA_OK) return rc;
+    if (!bytes || max_q_len < 0 || max_q_len > PA_MAX_TREE_ROWS) return PA_ERR_INVALID_ARG;
+    *bytes = pa::tree_ws_bytes(desc->head_dim);
+    return PA_OK;
+}
+
+int pa_decode_tree(void *out, const void *q, const int32_t *cu_q_lens, const int32_t *prefix_lens,
+                   const uint64_t *mask, const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                   int32_t num_q_heads, int32_t max_q_len, int32_t total_q_tokens, const void *k_cache,
+                   const void *v_cache, float scale, const float *k_scale, const float *v_scale, void *workspace,
+                   size_t workspace_bytes, const pa_cache_desc *desc, pa_stream_t stream) {
+    int rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    rc = check_attend(desc, num_seqs, max_blocks_per_seq, num_q_heads);
+    if (rc != PA_OK) return rc;
+    if (max_q_len < 0 || max_q_len > PA_MAX_TREE_ROWS || total_q_tokens < 0 ||
+        total_q_tokens > (int64_t)num_seqs * max_q_len || !(scale > 0.f) || scale > FLT_MAX)
+        return PA_ERR_INVALID_ARG;
+    const bool fp8 = desc->dtype == PA_DTYPE_FP8_E4M3;
+    if (fp8 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+    if (total_q_tokens == 0) return PA_OK;
+    if (!out || !q || !cu_q_lens || !prefix_lens || !mask || !block_tables || !k_cache || !v_cache)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    if (bad_workspace(workspace, workspace_bytes, pa::tree_ws_bytes(desc->head_dim))) return PA_ERR_WORKSPACE;
+    pa::TreeArgs a{out, q, cu_q_lens, prefix_lens, block_tables, mask, num_seqs, max_blocks_per_seq, num_q_heads,
+                   desc->num_kv_heads, desc->head_dim, max_q_len, total_q_tokens, desc->num_blocks, k_cache, v_cache,
+                   scale, fp8 ? k_scale : nullptr, fp8 ? v_scale : nullptr, fp8, status_word_ptr()};
+    return from_cuda(pa::launch_tree(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                     const pa_cache_desc *desc, size_t *bytes) {
+    int rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    rc = check_attend(desc, num_seqs, max_blocks_per_seq, num_q_heads);
+    if (rc != PA_OK) return rc;
+    if (!bytes) return PA_ERR_INVALID_ARG;
+    *bytes = pa::weights_ws_bytes(num_seqs, num_q_heads, desc->num_kv_heads, desc->head_dim, max_blocks_per_seq);
+    return PA_OK;
+}
+
+int pa_decode_weights(void *out, float *weights, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *block_tables, const int32_t *seq_lens, const int32_t *seen_lens,
+                      int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_q_heads, float scale,
+                      const float *k_scale, const float *v_scale, void *workspace, size_t workspace_bytes,
+                      const pa_cache_desc *desc, pa_stream_t stream) {
+    int rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    rc = check_attend(desc, num_seqs, max_blocks_per_seq, num_q_heads);
+    if (rc != PA_OK) return rc;
+    const bool fp8 = desc->dtype == PA_DTYPE_FP8_E4M3;
+    if (fp8 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !weights || !q || !k_cache || !v_cache || !block_tables || !seq_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(weights) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+        return PA_ERR_INVALID_ARG;
+    if (bad_workspace(workspace, workspace_bytes,
+                      pa::weights_ws_bytes(num_seqs, num_q_heads, desc->num_kv_heads, desc->head_dim,
+                                           max_blocks_per_seq)))
+        return PA_ERR_WORKSPACE;
+    pa::DecodeArgs a{out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, max_blocks_per_seq,
+                     num_q_heads, desc->num_kv_heads, desc->head_dim, desc->num_blocks, scale, k_scale, v_scale,
+                     0, 0, nullptr, nullptr, nullptr, fp8, status_word_ptr()};
+    return from_cuda(pa::launch_decode_weights(a, weights, seen_lens, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_select_tokens(int32_t *keep, int32_t *keep_lens, const float *weights, const int32_t *block_tables,
+                     const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t budget,
+                     int32_t num_sink, int32_t num_recent, const pa_cache_desc *desc, pa_stream_t stream) {
+    int rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks_per_seq <= 0 ||
+        max_blocks_per_seq > pa::kMaxBlocksPerSeq || budget <= 0 || budget > 16 * pa::kMaxBlocksPerSeq || num_sink < 0 || num_recent < 0 ||
+        (int64_t)num_sink + num_recent > budget)
+        return PA_ERR_INVALID_ARG;
+    if (desc->num_kv_heads > pa::kMaxDecodeKvHeads) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!keep || !keep_lens || !weights || !block_tables || !seq_lens || !aligned16(weights)) return PA_ERR_INVALID_ARG;
+    pa::SelectArgs a{keep, keep_lens, weights, block_tables, seq_lens, num_seqs, max_blocks_per_seq,
+                     desc->num_kv_heads, budget, num_sink, num_recent, desc->num_blocks, status_word_ptr()};
+    return from_cuda(pa::launch_select(a, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_compact_kv(void *k_cache, void *v_cache, float *weights, const int32_t *block_tables, const int32_t *keep,
+                  const int32_t *keep_lens, const int32_t *start_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
+                  int32_t keep_heads, int32_t max_keep, const pa_cache_desc *desc, pa_stream_t stream) {
+    int rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks_per_seq <= 0 ||
+        max_blocks_per_seq > pa::kMaxBlocksPerSeq || max_keep < 0 || max_keep > 16 * pa::kMaxBlocksPerSeq ||
+        (keep_heads != 1 && keep_heads != desc->num_kv_heads))
+        return PA_ERR_INVALID_ARG;
+    if (desc->num_kv_heads > pa::kMaxDecodeKvHeads) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_keep == 0) return PA_OK;
+    if (!k_cache || !v_cache || !block_tables || !keep || !keep_lens || !aligned16(k_cache) || !aligned16(v_cache))
+        return PA_ERR_INVALID_ARG;
+    pa::CompactArgs a{k_cache, v_cache, weights, block_tables, keep, keep_lens, start_lens, num_seqs,
+                      max_blocks_per_seq, desc->num_kv_heads, desc->head_dim, elem_bytes(desc), keep_heads, max_keep,
+                      desc->num_blocks, status_word_ptr()};
+    return from_cuda(pa::launch_compact(a, static_cast<cudaStream_t>(stream)));
 }
 
 int pa_get_last_device_error(uint32_t *flags, pa_stream_t stream) {

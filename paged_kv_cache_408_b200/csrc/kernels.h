@@ -80,11 +80,55 @@ struct PrefillArgs {
     bool fp8;
 };
 
+struct TreeArgs {
+    void *out;
+    const void *q;
+    const int32_t *cu_q, *prefix_lens, *block_tables;
+    const uint64_t *mask;  // [total_q]: bit j = the row sees draft j of its sequence
+    int B, max_blocks, Hq, Hkv, D, max_q_len, total_q;
+    int64_t num_blocks;
+    const void *k_cache, *v_cache;
+    float scale;
+    const float *k_scale, *v_scale;
+    bool fp8;
+    unsigned *err;
+};
+
+struct SelectArgs {
+    int32_t *keep, *keep_lens;  // [B][Hkv][budget], [B]
+    const float *weights;       // [num_blocks][Hkv][16]
+    const int32_t *block_tables, *seq_lens;
+    int B, max_blocks, Hkv, budget, sink, recent;
+    int64_t num_blocks;
+    unsigned *err;
+};
+
+struct CompactArgs {
+    void *k_cache, *v_cache;
+    float *weights;  // [num_blocks][Hkv][16] or nullptr
+    const int32_t *block_tables, *keep, *keep_lens, *start;  // start: nullptr = 0
+    int B, max_blocks, Hkv, D, elem_bytes, keep_heads, max_keep;
+    int64_t num_blocks;
+    unsigned *err;
+};
+
 cudaError_t launch_write_kv(const WriteArgs &a, cudaStream_t st);
 cudaError_t launch_copy_blocks(const CopyArgs &a, cudaStream_t st);
 // Returns cudaErrorNotSupported for a (head_dim, group, dtype) that is not built.
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t st);
+// Tree attention of drafted tokens (tree.cu).
+constexpr int kMaxTreeRows = 64;  // drafts of a sequence: the bits of a row's mask
+size_t tree_ws_bytes(int D);
+cudaError_t launch_tree(const TreeArgs &a, void *workspace, cudaStream_t st);
+// Decode that also adds every cached token's attention weight to a running
+// sum (weights.cu): weights [num_blocks][Hkv][16]; positions below seen[b]
+// are added to, the others start at zero (seen nullptr: all are added to).
+size_t weights_ws_bytes(int B, int Hq, int Hkv, int D, int max_blocks);
+cudaError_t launch_decode_weights(const DecodeArgs &a, float *weights, const int32_t *seen, void *workspace,
+                                  cudaStream_t st);
+cudaError_t launch_select(const SelectArgs &a, cudaStream_t st);
+cudaError_t launch_compact(const CompactArgs &a, cudaStream_t st);
 
 // Device address of the status word on the current device (nullptr if unknown).
 unsigned *status_word();

@@ -27,7 +27,10 @@ EXPORTED = (
     "pa_write_kv", "pa_copy_blocks", "pa_decode_workspace_size", "pa_decode", "pa_prefill_chunk",
     "pa_get_last_device_error", "pa_status_string", "pa_version", "pa_decode_noalloc",
     "pa_decode_cascade_workspace_size", "pa_decode_cascade",
+    "pa_decode_tree_workspace_size", "pa_decode_tree", "pa_decode_weights_workspace_size", "pa_decode_weights",
+    "pa_select_tokens", "pa_compact_kv",
 )
+MAX_TREE_ROWS = 64
 
 
 class PAError(RuntimeError):
@@ -64,6 +67,13 @@ def lib():
         L.pa_decode_cascade_workspace_size.argtypes = [i32, i32, i32, i32, C.POINTER(CacheDesc), C.POINTER(sz)]
         L.pa_decode_cascade.argtypes = [p, p, p, p, p, p, i32, i32, i32, f32, p, p, i32, p, sz,
                                         C.POINTER(CacheDesc), p]
+        D = C.POINTER(CacheDesc)
+        L.pa_decode_tree_workspace_size.argtypes = [i32, i32, i32, i32, D, C.POINTER(sz)]
+        L.pa_decode_tree.argtypes = [p, p, p, p, p, p, i32, i32, i32, i32, i32, p, p, f32, p, p, p, sz, D, p]
+        L.pa_decode_weights_workspace_size.argtypes = [i32, i32, i32, D, C.POINTER(sz)]
+        L.pa_decode_weights.argtypes = [p, p, p, p, p, p, p, p, i32, i32, i32, f32, p, p, p, sz, D, p]
+        L.pa_select_tokens.argtypes = [p, p, p, p, p, i32, i32, i32, i32, i32, D, p]
+        L.pa_compact_kv.argtypes = [p, p, p, p, p, p, p, i32, i32, i32, i32, D, p]
         L.pa_status_string.argtypes = [C.c_int]
         L.pa_status_string.restype = C.c_char_p
         for f in EXPORTED:
@@ -294,6 +304,153 @@ def prefill_chunk(out, q, cu_q_lens, prefix_lens, block_tables, k_cache, v_cache
         _ptr(out), _ptr(q), _ptr(cu_q_lens), _ptr(prefix_lens), _ptr(block_tables), n, block_tables.shape[1], Hq,
         int(max_q_len), total, _ptr(k_cache), _ptr(v_cache), float(scale), _ptr(ks), _ptr(vs), C.byref(desc),
         _stream(stream)))
+
+
+def tree_workspace_size(num_seqs, num_q_heads, max_q_len, max_blocks_per_seq, k_cache) -> int:
+    desc = cache_desc(k_cache)
+    out = C.c_size_t(0)
+    _check("pa_decode_tree_workspace_size", lib().pa_decode_tree_workspace_size(
+        int(num_seqs), int(num_q_heads), int(max_q_len), int(max_blocks_per_seq), C.byref(desc), C.byref(out)))
+    return int(out.value)
+
+
+def alloc_tree_workspace(num_seqs, num_q_heads, max_q_len, max_blocks_per_seq, k_cache):
+    """Caller-side helper: a torch buffer large enough for pa_decode_tree (no
+    particular contents needed)."""
+    n = tree_workspace_size(num_seqs, num_q_heads, max_q_len, max_blocks_per_seq, k_cache)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=k_cache.device)
+
+
+def decode_tree(out, q, cu_q_lens, prefix_lens, mask, block_tables, k_cache, v_cache, scale, max_q_len, workspace,
+                k_scale=None, v_scale=None, stream=None):
+    """pa_decode_tree: q, out bf16 [total_q, Hq, D]; cu_q_lens int32 [n+1];
+    prefix_lens int32 [n]; mask int64 (or uint64) [total_q], bit j = the row
+    sees draft j of its sequence; block_tables int32 [n, max_blocks]; at most
+    MAX_TREE_ROWS drafts a sequence."""
+    desc = _caches(k_cache, v_cache)
+    dev = k_cache.device
+    _need(q, "q", torch.bfloat16, dev)
+    _need(out, "out", torch.bfloat16, dev)
+    _need(cu_q_lens, "cu_q_lens", torch.int32, dev)
+    _need(prefix_lens, "prefix_lens", torch.int32, dev)
+    _need(mask, "mask", (torch.int64, torch.uint64), dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(workspace, "workspace", None, dev)
+    n = prefix_lens.numel()
+    if cu_q_lens.numel() != n + 1 or block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("cu_q_lens must be [n+1], block_tables [n, max_blocks]")
+    if q.dim() != 3 or out.shape != q.shape or q.shape[2] != desc.head_dim:
+        raise ValueError("out/q shape mismatch")
+    total, Hq, _ = q.shape
+    if mask.shape != (total,):
+        raise ValueError("mask must be [total_q]")
+    ks, vs = _scales(desc, k_scale, v_scale, dev)
+    _check("pa_decode_tree", lib().pa_decode_tree(
+        _ptr(out), _ptr(q), _ptr(cu_q_lens), _ptr(prefix_lens), _ptr(mask), _ptr(block_tables), n,
+        block_tables.shape[1], Hq, int(max_q_len), total, _ptr(k_cache), _ptr(v_cache), float(scale), _ptr(ks),
+        _ptr(vs), _ptr(workspace), workspace.numel() * workspace.element_size(), C.byref(desc), _stream(stream)))
+
+
+def _token_weights(weights, desc, device):
+    _need(weights, "weights", torch.float32, device)
+    if weights.shape != (desc.num_blocks, desc.num_kv_heads, BLOCK_SIZE):
+        raise ValueError(f"weights must be [num_blocks, Hkv, {BLOCK_SIZE}], got {tuple(weights.shape)}")
+
+
+def weights_workspace_size(num_seqs, num_q_heads, max_blocks_per_seq, k_cache) -> int:
+    desc = cache_desc(k_cache)
+    out = C.c_size_t(0)
+    _check("pa_decode_weights_workspace_size", lib().pa_decode_weights_workspace_size(
+        int(num_seqs), int(num_q_heads), int(max_blocks_per_seq), C.byref(desc), C.byref(out)))
+    return int(out.value)
+
+
+def alloc_weights_workspace(num_seqs, num_q_heads, max_blocks_per_seq, k_cache):
+    """Caller-side helper: a torch buffer large enough for pa_decode_weights
+    (no particular contents needed)."""
+    n = weights_workspace_size(num_seqs, num_q_heads, max_blocks_per_seq, k_cache)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=k_cache.device)
+
+
+def decode_weights(out, weights, q, k_cache, v_cache, block_tables, seq_lens, scale, workspace, seen_lens=None,
+                   k_scale=None, v_scale=None, stream=None):
+    """pa_decode_weights: decode that adds every cached token's attention
+    weight, summed over its kv head's query heads, to weights fp32
+    [num_blocks, Hkv, 16]; seen_lens int32 [B] (positions whose sum is there
+    already; None: all of them)."""
+    desc = _caches(k_cache, v_cache)
+    dev = k_cache.device
+    _need(q, "q", torch.bfloat16, dev)
+    _need(out, "out", torch.bfloat16, dev)
+    _token_weights(weights, desc, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    _need(workspace, "workspace", None, dev)
+    if q.dim() != 3 or out.shape != q.shape or q.shape[2] != desc.head_dim:
+        raise ValueError("out/q shape mismatch")
+    B, Hq, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
+    if seen_lens is not None:
+        _need(seen_lens, "seen_lens", torch.int32, dev)
+        if seen_lens.shape != (B,):
+            raise ValueError("seen_lens must be [B]")
+    ks, vs = _scales(desc, k_scale, v_scale, dev)
+    _check("pa_decode_weights", lib().pa_decode_weights(
+        _ptr(out), _ptr(weights), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(seen_lens), B, block_tables.shape[1], Hq, float(scale), _ptr(ks), _ptr(vs), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), C.byref(desc), _stream(stream)))
+
+
+def select_tokens(keep, keep_lens, weights, block_tables, seq_lens, num_sink, num_recent, stream=None):
+    """pa_select_tokens: the positions each kv head keeps under a budget
+    (keep int32 [B, Hkv, budget], ascending, then -1; keep_lens int32 [B]):
+    the first num_sink, the last num_recent, the heaviest of the rest by
+    weights fp32 [num_blocks, Hkv, 16]."""
+    _need(weights, "weights", torch.float32)
+    dev = weights.device
+    _need(keep, "keep", torch.int32, dev)
+    _need(keep_lens, "keep_lens", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    if weights.dim() != 3 or weights.shape[2] != BLOCK_SIZE:
+        raise ValueError(f"weights must be [num_blocks, Hkv, {BLOCK_SIZE}], got {tuple(weights.shape)}")
+    nb, hkv, bs = weights.shape
+    B = seq_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or keep_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, max_blocks], seq_lens and keep_lens [B]")
+    if keep.dim() != 3 or keep.shape[:2] != (B, hkv):
+        raise ValueError("keep must be [B, Hkv, budget]")
+    desc = CacheDesc(nb, hkv, bs, 128, DTYPE_BF16)  # the call reads num_blocks and num_kv_heads only
+    _check("pa_select_tokens", lib().pa_select_tokens(
+        _ptr(keep), _ptr(keep_lens), _ptr(weights), _ptr(block_tables), _ptr(seq_lens), B, block_tables.shape[1],
+        keep.shape[2], int(num_sink), int(num_recent), C.byref(desc), _stream(stream)))
+
+
+def compact_kv(k_cache, v_cache, block_tables, keep, keep_lens, weights=None, start_lens=None, stream=None):
+    """pa_compact_kv: K and V (and the weights, if given) of position
+    keep[b, head, i] move to position start_lens[b] + i, in place; keep int32
+    [B, Hkv or 1, max_keep] ascending, keep_lens int32 [B], start_lens int32
+    [B] (None: 0)."""
+    desc = _caches(k_cache, v_cache)
+    dev = k_cache.device
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(keep, "keep", torch.int32, dev)
+    _need(keep_lens, "keep_lens", torch.int32, dev)
+    B = keep_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [B, max_blocks]")
+    if keep.dim() != 3 or keep.shape[0] != B:
+        raise ValueError("keep must be [B, Hkv or 1, max_keep]")
+    if weights is not None:
+        _token_weights(weights, desc, dev)
+    if start_lens is not None:
+        _need(start_lens, "start_lens", torch.int32, dev)
+        if start_lens.shape != (B,):
+            raise ValueError("start_lens must be [B]")
+    _check("pa_compact_kv", lib().pa_compact_kv(
+        _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(block_tables), _ptr(keep), _ptr(keep_lens),
+        _ptr(start_lens), B, block_tables.shape[1], keep.shape[1], keep.shape[2], C.byref(desc), _stream(stream)))
 
 
 def get_last_device_error(stream=None) -> int:

@@ -74,10 +74,13 @@ constexpr int kSegmentCost = 2;            // balanced split: cost units charged
 constexpr size_t kRingBytes = 192 * 1024;  // K/V staging rings of all warps of an SM
 constexpr unsigned kFull = 0xffffffffu;
 
-template <int D_, int G_, bool FP8_>
+template <int D_, int G_, bool FP8_, bool W_ = false>
 struct Cfg {
     static constexpr int D = D_, G = G_;
     static constexpr bool FP8 = FP8_;
+    // leave every token's scores and every piece's log2-sum-exp in the
+    // workspace, for the attention weights (weights.cu)
+    static constexpr bool W = W_;
     static constexpr int EB = FP8 ? 1 : 2;           // bytes per element
     static constexpr int DPL = (G >= 4) ? 8 : 16;     // head dims owned by a lane
     static constexpr int LPT = D / DPL;               // lanes per token
@@ -437,6 +440,21 @@ struct QPrefetch {
     }
 };
 
+// Where a piece's fp32 output and log2-sum-exp go: head h of the group is row
+// base + h * stride of ws_o and ws_lse.
+struct PieceAt {
+    size_t base, stride;
+};
+
+template <class C>
+PA_DEVICE PieceAt piece_at(const DecodeArgs &a, const Item &it, size_t row0, int gw) {
+    // of the cut segments that a warp meets, only its last one can begin in
+    // its share, and only its first one before it: two slots a warp hold
+    // every piece, piece p of a segment in warp ws_first + p's
+    if constexpr (C::W) return {((size_t)gw * 2 + (it.piece == 0 ? 1 : 0)) * C::G, 1};
+    return {row0 * a.max_parts + it.piece + a.prefix_pieces, (size_t)a.max_parts};
+}
+
 // ---- tensor-core decode (fp8 cache, GQA groups of 8) ----------------------
 //
 // With an fp8 cache and 8 q heads per kv head, q.k and p.v on CUDA cores
@@ -506,7 +524,7 @@ struct QPrefetchMma {
 template <class C>
 PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &prod, ItemIter &items,
                          uint8_t *my_stages, uint64_t *my_bars, int *my_valid, int lane, const uint8_t *kc,
-                         const uint8_t *vc, uint64_t deadline) {
+                         const uint8_t *vc, uint64_t deadline, int gw) {
     constexpr int D = C::D, G = C::G, NK = D / 16, NM = D / 16, KW = D / 16, VB = D / 8;
     static_assert(C::FP8 && G == 8, "tensor-core decode: fp8 cache, GQA 8");
     const int r = lane >> 2, c = lane & 3, Hkv = sc.Hkv;
@@ -599,6 +617,10 @@ PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &p
             const bool ok0 = r < valid, ok8 = r + 8 < valid;
             const float t0 = ok0 ? st[0] * sl2 : -INFINITY, t1 = ok0 ? st[1] * sl2 : -INFINITY;
             const float t2 = ok8 ? st[2] * sl2 : -INFINITY, t3 = ok8 ? st[3] * sl2 : -INFINITY;
+            if constexpr (C::W) {  // scores of heads 2c, 2c+1 of tokens r and r + 8
+                float *sw = a.scores + (((size_t)it.b * Hkv + it.kvh) * a.max_blocks + it.blk0 + j) * 16 * G + 32 * c + r;
+                sw[0] = t0, sw[16] = t1, sw[8] = t2, sw[24] = t3;
+            }
             const bool need = fmaxf(t0, t2) > m0 + kRescaleThreshold || fmaxf(t1, t3) > m1 + kRescaleThreshold;
             if (__any_sync(kFull, need)) {
                 float b0 = fmaxf(t0, t2), b1 = fmaxf(t1, t3);
@@ -670,13 +692,17 @@ PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &p
 #pragma unroll
                 for (int i = 0; i < VB / 8; ++i) dst[i] = make_uint4(wds[4 * i], wds[4 * i + 1], wds[4 * i + 2], wds[4 * i + 3]);
             }
+            if (C::W && r == 0) {
+                a.ws_row_lse[row0 + 2 * c] = (l0 > 0.f) ? m0 + lg2(l0) : -INFINITY;
+                a.ws_row_lse[row0 + 2 * c + 1] = (l1 > 0.f) ? m1 + lg2(l1) : -INFINITY;
+            }
             if (lane == 0 && a.ws_np) a.ws_np[(size_t)it.b * Hkv + it.kvh] = 1;
         } else {
-            const int piece = it.piece + a.prefix_pieces;
+            const PieceAt at = piece_at<C>(a, it, row0, gw);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 const float inv = hh ? inv1 : inv0;
-                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + ((row0 + 2 * c + hh) * a.max_parts + piece) * D + r * VB);
+                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + (at.base + (2 * c + hh) * at.stride) * D + r * VB);
 #pragma unroll
                 for (int i = 0; i < VB / 4; ++i) {
                     float v[4];
@@ -689,10 +715,13 @@ PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &p
                 }
             }
             if (r == 0) {
-                a.ws_lse[(row0 + 2 * c) * a.max_parts + piece] = (l0 > 0.f) ? m0 + lg2(l0) : -INFINITY;
-                a.ws_lse[(row0 + 2 * c + 1) * a.max_parts + piece] = (l1 > 0.f) ? m1 + lg2(l1) : -INFINITY;
+                a.ws_lse[at.base + 2 * c * at.stride] = (l0 > 0.f) ? m0 + lg2(l0) : -INFINITY;
+                a.ws_lse[at.base + (2 * c + 1) * at.stride] = (l1 > 0.f) ? m1 + lg2(l1) : -INFINITY;
             }
-            if (lane == 0 && it.piece == 0) a.ws_np[(size_t)it.b * Hkv + it.kvh] = it.npieces + a.prefix_pieces;
+            if (lane == 0 && it.piece == 0) {
+                a.ws_np[(size_t)it.b * Hkv + it.kvh] = it.npieces + a.prefix_pieces;
+                if constexpr (C::W) a.ws_first[(size_t)it.b * Hkv + it.kvh] = gw;
+            }
         }
         it = nx;
         have = have_nx;
@@ -715,7 +744,8 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int g = lane / LPT, sub = lane % LPT;
     const int B = a.B, Hkv = a.Hkv, P = a.partition_tokens;  // P == 0: balanced split
-    const int gw = blockIdx.x * NW + w, GW = gridDim.x * NW;
+    // (with scores the shares are small in a small batch: neighbours go to different SMs)
+    const int gw = C::W ? w * gridDim.x + blockIdx.x : blockIdx.x * NW + w, GW = gridDim.x * NW;
     pdl_trigger();  // the merge kernel may be scheduled now; it waits for this grid
     pdl_wait();     // the preceding kernel (e.g. the K/V write) has completed
     const uint64_t deadline = wait_deadline();  // shared by every wait of this launch
@@ -796,7 +826,7 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
     sc.P = P;
     if (P == 0) {
         sc.total = s_pre0[B];
-        sc.S = max((sc.total + GW - 1) / GW, kMinShareBlocks);
+        sc.S = max((sc.total + GW - 1) / GW, C::W ? kMinScoreShare : kMinShareBlocks);
         sc.NF = 0;
     } else {
         sc.NF = s_pre0[B];
@@ -840,7 +870,7 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
     ItemIter items;
     items.start(sc, gw, GW);
     if constexpr (C::MMA) {
-        mma_items<C>(a, sc, prod, items, my_stages, my_bars, my_valid, lane, kc, vc, deadline);
+        mma_items<C>(a, sc, prod, items, my_stages, my_bars, my_valid, lane, kc, vc, deadline, gw);
     } else {
         Item it, nx;
         bool have = items.next(sc, it);
@@ -912,6 +942,10 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                         const int t = t_base + C::NGRP * ((i / G) ^ sj);
                         sco[i] = (t < valid) ? part[i] : -INFINITY;
                         need |= sco[i] > m[i % G] + kRescaleThreshold;
+                        if constexpr (C::W)
+                            if (C::RS || sub == i % LPT)  // (else every lane of the group holds every score)
+                                a.scores[(((size_t)it.b * Hkv + it.kvh) * a.max_blocks + it.blk0 + j) * 16 * G +
+                                         ((i % G) ^ sh) * 16 + t] = sco[i];
                     }
                     if (__any_sync(kFull, need)) {
                         float bm[G];
@@ -988,6 +1022,8 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                             }
                             *reinterpret_cast<uint4 *>(dst + choff[c] * 8) = make_uint4(wds[0], wds[1], wds[2], wds[3]);
                         }
+                        if (C::W && sub == 0)
+                            a.ws_row_lse[row0 + h] = (l[h] > 0.f) ? m[h] + lg2(l[h]) : -INFINITY;
                     }
                 }
                 if (lane == 0 && a.ws_np) a.ws_np[(size_t)it.b * Hkv + it.kvh] = 1;  // nothing to merge
@@ -995,12 +1031,12 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                 // ---- split-K: this piece's normalised output and log2-sum-exp;
                 // piece 0 also records how many pieces the merge kernel combines
                 // (in a cascade the pieces follow the shared prefix's pieces)
-                const int piece = it.piece + a.prefix_pieces;
+                const PieceAt at = piece_at<C>(a, it, row0, gw);
                 if (g == 0) {
     #pragma unroll
                     for (int h = 0; h < G; ++h) {
                         const float inv = (l[h] > 0.f) ? vscale / l[h] : 0.f;
-                        float *dst = a.ws_o + ((row0 + (h ^ sh)) * a.max_parts + piece) * D;
+                        float *dst = a.ws_o + (at.base + (h ^ sh) * at.stride) * D;
     #pragma unroll
                         for (int c = 0; c < C::NCH; ++c) {
                             float4 *d4 = reinterpret_cast<float4 *>(dst + choff[c] * 8);
@@ -1010,11 +1046,13 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                                                 acc2[h][4 * c + 3].x * inv, acc2[h][4 * c + 3].y * inv);
                         }
                         if (sub == 0)  // sub 0 has sh == 0: slot h is head h
-                            a.ws_lse[(row0 + h) * a.max_parts + piece] = (l[h] > 0.f) ? m[h] + lg2(l[h]) : -INFINITY;
+                            a.ws_lse[at.base + h * at.stride] = (l[h] > 0.f) ? m[h] + lg2(l[h]) : -INFINITY;
                     }
                 }
-                if (lane == 0 && it.piece == 0)
+                if (lane == 0 && it.piece == 0) {
                     a.ws_np[(size_t)it.b * Hkv + it.kvh] = it.npieces + a.prefix_pieces;
+                    if constexpr (C::W) a.ws_first[(size_t)it.b * Hkv + it.kvh] = gw;
+                }
             }
             it = nx;
             have = have_nx;
@@ -1166,8 +1204,13 @@ cudaError_t run(const DecodeArgs &a, cudaStream_t st) {
     const long long units = a.partition_tokens == 0
                                 ? (long long)a.Hkv * a.B * (a.max_blocks + kSegmentCost) / kMinShareBlocks + 1
                                 : (long long)a.Hkv * a.B * a.max_parts;
-    const long long grid = std::max<long long>(1, std::min<long long>((units + C::NW - 1) / C::NW, ctas));
+    long long grid = std::max<long long>(1, std::min<long long>((units + C::NW - 1) / C::NW, ctas));
+    if (C::W) {  // a warp a CTA before a CTA fills up, and no more warps than the workspace has slots for
+        const long long shares = (long long)a.Hkv * a.B * (a.max_blocks + kSegmentCost) / kMinScoreShare + 1;
+        grid = std::min<long long>({shares, ctas, kMaxScoreWarps / C::NW});
+    }
     e = launch_pdl(decode_kernel<C>, dim3((unsigned)grid), dim3(C::NT), smem, st, a);
+    if (C::W) return e;                          // weights.cu merges
     if (e != cudaSuccess || !a.ws_np) return e;  // no workspace: every (sequence, kv head) is one piece
     const long long rows = (long long)a.B * a.Hq;
     DecodeArgs m = a;
@@ -1178,13 +1221,13 @@ cudaError_t run(const DecodeArgs &a, cudaStream_t st) {
     return launch_pdl(merge_kernel<C::D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, m);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool W = false>
 cudaError_t by_group(const DecodeArgs &a, cudaStream_t st) {
     switch (a.Hq / a.Hkv) {
-        case 1: return run<Cfg<D, 1, FP8>>(a, st);
-        case 2: return run<Cfg<D, 2, FP8>>(a, st);
-        case 4: return run<Cfg<D, 4, FP8>>(a, st);
-        case 8: return run<Cfg<D, 8, FP8>>(a, st);
+        case 1: return run<Cfg<D, 1, FP8, W>>(a, st);
+        case 2: return run<Cfg<D, 2, FP8, W>>(a, st);
+        case 4: return run<Cfg<D, 4, FP8, W>>(a, st);
+        case 8: return run<Cfg<D, 8, FP8, W>>(a, st);
         default: return cudaErrorNotSupported;
     }
 }
@@ -1213,6 +1256,12 @@ void decode_ws_carve(void *base, int B, int Hq, int D, int max_parts, DecodeArgs
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t st) {
     if (a.D == 128) return a.fp8 ? by_group<128, true>(a, st) : by_group<128, false>(a, st);
     if (a.D == 64) return a.fp8 ? by_group<64, true>(a, st) : by_group<64, false>(a, st);
+    return cudaErrorNotSupported;
+}
+
+cudaError_t launch_decode_scores(const DecodeArgs &a, cudaStream_t st) {
+    if (a.D == 128) return a.fp8 ? by_group<128, true, true>(a, st) : by_group<128, false, true>(a, st);
+    if (a.D == 64) return a.fp8 ? by_group<64, true, true>(a, st) : by_group<64, false, true>(a, st);
     return cudaErrorNotSupported;
 }
 

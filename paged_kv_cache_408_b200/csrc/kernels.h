@@ -51,6 +51,12 @@ struct DecodeArgs {
     int prefix_pieces;
     int merge_spec;        // pieces the merge kernel loads per row before it has read the row's piece count
                            // (set by the decode launcher)
+    // launch_decode_scores: scores in log2 units [B][Hkv][max_blocks][Hq/Hkv][16]; the log2-sum-exp of rows of
+    // one piece [B][Hq]; the warp that holds a cut (sequence, kv head)'s first piece [B][Hkv].  ws_o and ws_lse
+    // are then [2 kMaxScoreWarps][Hq/Hkv][D] and [..][Hq/Hkv]: slot 2 w + 1 holds warp w's piece 0 of a cut
+    // segment, slot 2 w its later piece of one.
+    float *scores, *ws_row_lse;
+    int *ws_first;
 };
 
 struct PrefillArgs {
@@ -116,6 +122,10 @@ cudaError_t launch_write_kv(const WriteArgs &a, cudaStream_t st);
 cudaError_t launch_copy_blocks(const CopyArgs &a, cudaStream_t st);
 // Returns cudaErrorNotSupported for a (head_dim, group, dtype) that is not built.
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t st);
+// The decode kernel alone (balanced split, no cascade): it also leaves every
+// token's scores, and the log2-sum-exp of every piece, single ones included.
+// Rows of one piece are written to out, the others' pieces are not merged.
+cudaError_t launch_decode_scores(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t st);
 // Tree attention of drafted tokens (tree.cu).
 constexpr int kMaxTreeRows = 64;  // drafts of a sequence: the bits of a row's mask
@@ -145,6 +155,8 @@ int sm_count();
 constexpr int kMaxDecodeSeqs = 2048;
 constexpr int kMinShareBlocks = 16;  // balanced split: smallest per-warp share, in cost units
 constexpr int kMaxDecodeKvHeads = 128;
+constexpr int kMinScoreShare = 4;     // the same for launch_decode_scores, whose pieces take no room by their count
+constexpr int kMaxScoreWarps = 1920;  // launch_decode_scores: most warps (12 an SM, 148 SMs)
 // Widest block table any entry point accepts (PA_MAX_BLOCKS_PER_SEQ): token
 // positions (16 * max_blocks) and piece counts stay far inside int32.
 constexpr int kMaxBlocksPerSeq = PA_MAX_BLOCKS_PER_SEQ;

@@ -6,116 +6,218 @@
 //     p_h(t) = 2^(s_h(t) - L_h),  s = scale log2(e) q_h . k_t,
 //     L_h the log2-sum-exp of s_h over the sequence.
 //
-// Two kernels: one warp per (sequence, query head) attends and leaves L_h;
-// then one warp per (sequence, kv head, block) computes the scores again.
+// A weight needs its row's whole sum, so it takes a second pass over the
+// scores.  The decode kernel (its balanced split and streaming unchanged)
+// leaves them in the workspace in fp32, 4 B a token and query head against
+// 2 D bytes a token and kv head (E4M3; 4 D for bf16) of K and V: reading K
+// again instead would cost D (2 D) bytes a token and kv head.  fp32, because
+// the sums that selection compares are fp32: a score rounded to f16 would
+// move a weight by up to |s| 2^-11.
+// The finishing kernel, a programmatic dependent, has for each (sequence, kv
+// head) CTAs that merge the pieces' outputs and, to add the weights, CTAs
+// that take a share of the tokens: the pieces' log2-sum-exps give
+// L_h, and each thread updates 4 tokens at a time (16 B of sums, 16 G B of
+// scores, loaded before L_h is known).
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace pa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTokens = 4 * kThreads;  // tokens a CTA updates per step
 
-template <int E, bool FP8>
-PA_DEVICE void load_dims(const void *cache, size_t at, float (&x)[E]) {
-    for (int e = 0; e < E; ++e) {
-        if constexpr (FP8) x[e] = (float)static_cast<const __nv_fp8_e4m3 *>(cache)[at + e];
-        else x[e] = __bfloat162float(static_cast<const __nv_bfloat16 *>(cache)[at + e]);
-    }
+// log2-sum-exp over the pieces of one row, by one warp: the pieces' values
+// at lse[slot(p) * G].
+PA_DEVICE int piece_slot(int first, int p) { return (first + p) * 2 + (p == 0 ? 1 : 0); }
+
+template <int G>
+PA_DEVICE float row_lse(const float *lse, int first, int np, int lane) {
+    float m = -INFINITY, l = 0.f;
+    for (int p = lane; p < np; p += 32) m = fmaxf(m, __ldcg(lse + (size_t)piece_slot(first, p) * G));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float mb = m == -INFINITY ? 0.f : m;
+    for (int p = lane; p < np; p += 32) l += ex2(__ldcg(lse + (size_t)piece_slot(first, p) * G) - mb);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    return l > 0.f ? mb + lg2(l) : INFINITY;  // no weight at all: 2^-inf = 0 for every token
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(128) attend_kernel(const DecodeArgs a, float *lse) {
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads) finish_kernel(const DecodeArgs a, float *__restrict__ weights,
+                                                          const int32_t *__restrict__ seen, int mc) {
     constexpr int E = D / 32;
+    __shared__ float s_lse[G];
+    __shared__ float s_acc[kWarps][D];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int kvh = blockIdx.y, b = blockIdx.z;
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (long long)a.B * a.Hq) return;
-    const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), kvh = h / (a.Hq / a.Hkv);
-    int len = a.seq_lens[b];
-    if (len < 0 || len > a.max_blocks * 16) {
-        if (lane == 0) flag_error(a.err, PA_DEVERR_BAD_LEN);
-        len = 0;
-    }
-    float q[E], acc[E], m = -INFINITY, l = 0.f;
-    const float sl2 = a.scale * kLog2e * (FP8 ? a.k_scale[kvh] : 1.f);
-    load_dims<E, false>(a.q, row * D + lane * E, q);
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int t = 0; t < len; ++t) {
-        const int64_t blk = a.block_tables[(size_t)b * a.max_blocks + (t >> 4)];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) flag_error(a.err, PA_DEVERR_BAD_BLOCK);
-            continue;
-        }
-        const size_t at = ((blk * a.Hkv + kvh) * 16 + (t & 15)) * D + lane * E;
-        float k[E], v[E], s = 0.f;
-        load_dims<E, FP8>(a.k_cache, at, k);
-        load_dims<E, FP8>(a.v_cache, at, v);
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= sl2;
-        const float mn = fmaxf(m, s), al = mn == -INFINITY ? 1.f : ex2(m - mn), p = mn == -INFINITY ? 0.f : ex2(s - mn);
-        m = mn;
-        l = l * al + p;
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * al + p * v[e];
-    }
-    const float inv = (l > 0.f ? 1.f / l : 0.f) * (FP8 ? a.v_scale[kvh] : 1.f);
-    for (int e = 0; e < E; ++e)
-        static_cast<__nv_bfloat16 *>(a.out)[row * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
-    if (lane == 0) lse[row] = l > 0.f ? m + log2f(l) : INFINITY;  // no token: every weight 2^-inf = 0
-}
-
-template <int D, bool FP8>
-__global__ void __launch_bounds__(128) add_kernel(const DecodeArgs a, const float *lse, float *w, const int32_t *seen) {
-    constexpr int E = D / 32;
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
-    const long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int j = (int)(u % a.max_blocks), kvh = (int)(u / a.max_blocks % a.Hkv), b = (int)(u / a.max_blocks / a.Hkv);
-    if (b >= a.B) return;
+    const size_t seg = (size_t)b * a.Hkv + kvh, row0 = (size_t)b * a.Hq + (size_t)kvh * G;
     const int len = a.seq_lens[b];
-    if (len > a.max_blocks * 16 || j * 16 >= len) return;
-    const int64_t blk = a.block_tables[(size_t)b * a.max_blocks + j];
-    if (blk < 0 || blk >= a.num_blocks) return;
-    const float sl2 = a.scale * kLog2e * (FP8 ? a.k_scale[kvh] : 1.f);
-    const int old = seen ? seen[b] : len;
-    for (int i = 0; i < 16 && j * 16 + i < len; ++i) {
-        const size_t slot = (blk * a.Hkv + kvh) * 16 + i;
-        float k[E], sum = 0.f;
-        load_dims<E, FP8>(a.k_cache, slot * D + lane * E, k);
-        for (int g = 0; g < G; ++g) {
-            const size_t row = (size_t)b * a.Hq + kvh * G + g;
-            float q[E], s = 0.f;
-            load_dims<E, false>(a.q, row * D + lane * E, q);
-            for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            sum += exp2f(s * sl2 - lse[row]);
+    const int np = __ldcg(a.ws_np + seg);
+    if (len <= 0 || len > a.max_blocks * 16) return;  // the decode kernel wrote the rows (and flagged a bad length)
+    const int first = np > 1 ? __ldcg(a.ws_first + seg) : 0;
+    const bool ok = np >= 1 && first >= 0 && first + np <= kMaxScoreWarps;  // else the decode kernel gave up (flagged)
+
+    if ((int)blockIdx.x < mc) {  // ---- merge the pieces of G / mc heads: sum_p 2^(lse_p - L) o_p
+        if (np == 1 || !ok) return;  // the decode kernel wrote the rows
+        const int heads = G / mc, per = kWarps / heads;  // `per` warps a head, each every per-th piece
+        const int h = blockIdx.x * heads + w / per;
+        const float *lse = a.ws_lse + h, *op = a.ws_o + (size_t)h * D + lane * E;
+        const float L = row_lse<G>(lse, first, np, lane);
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int p = w % per; p < np; p += per) {
+            const size_t at = (size_t)piece_slot(first, p) * G;
+            const float wt = ex2(__ldcg(lse + at) - L);
+            float v[E];
+            if constexpr (E == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(op + at * D));
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(op + at * D));
+                v[0] = x.x, v[1] = x.y;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[e], acc[e]);
         }
-        if (lane == 0) w[slot] = (j * 16 + i < old ? w[slot] : 0.f) + sum;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_acc[w][lane * E + e] = acc[e];
+        __syncthreads();
+        for (int i = tid; i < heads * D / 2; i += kThreads) {
+            const int hh = i / (D / 2), d = i % (D / 2) * 2;
+            float x = 0.f, y = 0.f;
+            for (int k = hh * per; k < (hh + 1) * per; ++k) x += s_acc[k][d], y += s_acc[k][d + 1];
+            reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                               (row0 + blockIdx.x * heads + hh) * D)[d / 2] = __floats2bfloat162_rn(x, y);
+        }
+        return;
+    }
+
+    // ---- add the weights
+    const int t0 = (((int)blockIdx.x - mc) * kThreads + tid) * 4, step = ((int)gridDim.x - mc) * kTokens;
+    if (t0 - tid * 4 >= len) return;  // (uniform)
+    const float *sc = a.scores + seg * a.max_blocks * 16 * G;
+    const int32_t *bt = a.block_tables + (size_t)b * a.max_blocks;
+    const int old = seen ? seen[b] : len;
+    float s[G][4], x[4];
+    float *slot = nullptr;
+    auto load = [&](int t) {
+        const int64_t blk = bt[t >> 4];
+        slot = nullptr;
+        if (blk < 0 || blk >= a.num_blocks) return;  // flagged by the decode kernel
+        slot = weights + (blk * a.Hkv + kvh) * 16 + (t & 15);
+        const float *src = sc + (size_t)(t >> 4) * 16 * G + (t & 15);
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + h * 16));
+            s[h][0] = v.x, s[h][1] = v.y, s[h][2] = v.z, s[h][3] = v.w;
+        }
+        const float4 v = *reinterpret_cast<const float4 *>(slot);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    };
+    if (t0 < len) load(t0);  // the first step's loads do not wait for the sums
+    if (!ok) return;
+    for (int h = w; h < G; h += kWarps) {
+        const float L = np > 1 ? row_lse<G>(a.ws_lse + h, first, np, lane) : __ldcg(a.ws_row_lse + row0 + h);
+        if (lane == 0) s_lse[h] = L == -INFINITY ? INFINITY : L;
+    }
+    __syncthreads();
+    float L[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) L[h] = s_lse[h];
+    for (int t = t0; t < len; t += step) {
+        if (t > t0) load(t);
+        if (!slot) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float sum = 0.f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) sum += ex2(s[h][i] - L[h]);
+            x[i] = (t + i < old ? x[i] : 0.f) + sum;
+        }
+        if (t + 4 <= len) {
+            *reinterpret_cast<float4 *>(slot) = make_float4(x[0], x[1], x[2], x[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (t + i < len) slot[i] = x[i];
+        }
     }
 }
 
-template <int D, bool FP8>
-cudaError_t run(const DecodeArgs &a, float *weights, const int32_t *seen, float *lse, cudaStream_t st) {
-    const long long rows = (long long)a.B * a.Hq, blocks = (long long)a.B * a.Hkv * a.max_blocks;
-    cudaError_t e = launch_pdl(attend_kernel<D, FP8>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a, lse);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(add_kernel<D, FP8>, dim3((unsigned)((blocks + 3) / 4)), dim3(128), 0, st, a, (const float *)lse,
-                      weights, seen);
+template <int D, int G>
+cudaError_t finish(const DecodeArgs &a, float *weights, const int32_t *seen, cudaStream_t st) {
+    // CTAs per (sequence, kv head): with few of them each is cut into many
+    // pieces, so a CTA merges one head; with many, one merges all heads.
+    // Token shares: as many as the tokens fill, within one wave of the grid.
+    const long long rows = (long long)a.B * a.Hkv, wave = 2048 / kThreads * (long long)sm_count();
+    const int mc = rows < sm_count() ? G : 1;
+    const long long cx = std::min<long long>(std::max<long long>(1, wave / rows - mc),
+                                             ((long long)a.max_blocks * 16 + kTokens - 1) / kTokens);
+    return launch_pdl(finish_kernel<D, G>, dim3((unsigned)(cx + mc), a.Hkv, a.B), dim3(kThreads), 0, st, a, weights, seen,
+                      mc);
+}
+
+template <int D>
+cudaError_t finish_by_group(const DecodeArgs &a, float *weights, const int32_t *seen, cudaStream_t st) {
+    switch (a.Hq / a.Hkv) {
+        case 1: return finish<D, 1>(a, weights, seen, st);
+        case 2: return finish<D, 2>(a, weights, seen, st);
+        case 4: return finish<D, 4>(a, weights, seen, st);
+        case 8: return finish<D, 8>(a, weights, seen, st);
+        default: return cudaErrorNotSupported;
+    }
 }
 
 }  // namespace
 
-size_t weights_ws_bytes(int B, int Hq, int, int, int) { return (size_t)B * Hq * sizeof(float); }
+namespace {
 
-cudaError_t launch_decode_weights(const DecodeArgs &a, float *weights, const int32_t *seen, void *workspace,
+// The workspace: piece counts, first warps, log2-sum-exps of whole rows,
+// pieces, scores; every region 256-byte aligned.
+struct Layout {
+    size_t np, first, row, o, lse, scores, total;
+};
+
+Layout layout(int B, int Hq, int Hkv, int D, int max_blocks) {
+    auto round256 = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    const size_t slots = 2 * (size_t)kMaxScoreWarps * (Hq / Hkv);
+    Layout l{};
+    l.first = l.np + round256((size_t)B * Hkv * 4);
+    l.row = l.first + round256((size_t)B * Hkv * 4);
+    l.o = l.row + round256((size_t)B * Hq * 4);
+    l.lse = l.o + slots * D * 4;
+    l.scores = l.lse + round256(slots * 4);
+    l.total = l.scores + (size_t)B * Hq * max_blocks * 16 * 4;
+    return l;
+}
+
+}  // namespace
+
+size_t weights_ws_bytes(int B, int Hq, int Hkv, int D, int max_blocks) { return layout(B, Hq, Hkv, D, max_blocks).total; }
+
+cudaError_t launch_decode_weights(const DecodeArgs &d, float *weights, const int32_t *seen, void *workspace,
                                   cudaStream_t st) {
-    float *lse = static_cast<float *>(workspace);
-    if (a.D == 128) return a.fp8 ? run<128, true>(a, weights, seen, lse, st) : run<128, false>(a, weights, seen, lse, st);
-    if (a.D == 64) return a.fp8 ? run<64, true>(a, weights, seen, lse, st) : run<64, false>(a, weights, seen, lse, st);
-    return cudaErrorNotSupported;
+    DecodeArgs a = d;
+    const Layout l = layout(a.B, a.Hq, a.Hkv, a.D, a.max_blocks);
+    char *ws = static_cast<char *>(workspace);
+    a.partition_tokens = 0;
+    a.ws_np = reinterpret_cast<int *>(ws + l.np);
+    a.ws_first = reinterpret_cast<int *>(ws + l.first);
+    a.ws_row_lse = reinterpret_cast<float *>(ws + l.row);
+    a.ws_o = reinterpret_cast<float *>(ws + l.o);
+    a.ws_lse = reinterpret_cast<float *>(ws + l.lse);
+    a.scores = reinterpret_cast<float *>(ws + l.scores);
+    const cudaError_t e = launch_decode_scores(a, st);
+    if (e != cudaSuccess) return e;
+    return a.D == 128 ? finish_by_group<128>(a, weights, seen, st) : finish_by_group<64>(a, weights, seen, st);
 }
 
 }  // namespace pa

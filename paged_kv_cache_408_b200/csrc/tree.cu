@@ -8,28 +8,31 @@
 //     out = sum_t softmax_t(scale q . k_t) v_t    over those keys,
 // zero where there are none.
 //
-// Work split: a segment is (sequence, kv head, row tile), a row tile being
-// 128 accumulator rows = 128/G drafts x the G query heads of a kv head, so
-// K and V are read from HBM once per sequence (a second row tile, T G > 128,
-// finds them in L2).  The segments' key tiles (128 keys, 8 blocks) form one
-// line, kSegCost units at the head of each segment and one per tile, cut
-// into equal contiguous shares, one per SM.  Of the segments a CTA meets
-// only its first can have begun before its share and only its last can go
-// on behind it, so two slots a CTA hold every partial result, whatever the
-// batch; the merge kernel joins them by log-sum-exp.
+// Work split: a row tile is 128 accumulator rows = 128/G drafts x the G query
+// heads of a kv head; a segment is (sequence, kv head, one or two row tiles),
+// so K and V are read from HBM once per sequence (further segments, T G >
+// 256, find them in L2).  The segments' key tiles (128 keys, 8 blocks) form
+// one line of cost units (kSegCost at the head of a segment, kOne or kPair a
+// tile), cut into equal contiguous shares, one per SM.  Of the segments a
+// CTA meets only its first can have begun before its share and only its last
+// can go on behind it, so two slots a CTA hold every partial result, whatever
+// the batch; the merge kernel joins them by log-sum-exp.
 //
-// Within a CTA: a loader warp gathers K and V tiles through the block table
-// (2-D TMA boxes, 128-byte swizzle) into two rings; one thread issues the
-// MMAs; two softmax warpgroups take the key tiles in turn, each with its own
-// score buffer, running maximum, sum and output accumulator in TMEM (a
-// thread owns a whole row of 128 scores: no exchange between threads until
-// the end of the segment, where the two accumulators are joined).  Scores of
-// tile n+1 are computed while the exponentials of tile n run.  P is written
-// over its scores in TMEM and is the A operand of P.V.  Warps whose 32 rows
-// are all past the drafts skip the arithmetic.
+// Within a CTA the work is a line of steps, each the scores, softmax and P.V
+// of one row tile and one key tile; steps alternate between two streams, each
+// with its own score buffer and output accumulator in TMEM and its own softmax
+// warpgroup (a thread owns a whole row of 128 scores: no exchange between
+// threads).  A segment of two row tiles has one on each stream, sharing the K
+// and V tiles; of one row tile the streams take the key tiles in turn, and the
+// two accumulators are joined at the end.  A loader warp gathers K and V tiles
+// through the block table (2-D TMA boxes, 128-byte swizzle) into two rings;
+// one thread issues the MMAs, the scores of step n+1 before P.V of step n, so
+// that the tensor pipe works while the exponentials run.  P is written over
+// its scores in TMEM and is the A operand of P.V.  Warps whose 32 rows are all
+// past the drafts skip the arithmetic.
 // An E4M3 cache: the codes land in a staging ring and four warps widen them
-// exactly to f16 operand tiles; the query rows are scaled by a power of two
-// into f16's range.
+// to f16 operand tiles; the query rows are scaled by a power of two into
+// f16's range.
 // Bound: HBM for up to 128 rows a kv head (the tensor pipe then needs about
 // a third of the time that the K and V bytes take), the tensor and softmax
 // pipes beyond.
@@ -47,7 +50,9 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the running maximum may lag behind
-constexpr int kSegCost = 1;                // units charged per segment (query tile, epilogue)
+// line units: per segment (epilogue, first tile), per key tile of a segment
+// of one and of two row tiles
+constexpr int kSegCost = 4, kOne = 2, kPair = 3;
 constexpr int kMaxCtas = 160;              // partial-result slots: two a CTA
 constexpr int kEpiBar = 1;                 // named barrier of the softmax warps
 constexpr unsigned kFull = 0xffffffffu;
@@ -61,75 +66,93 @@ struct TCfg {
     static constexpr int NATOM = D / 64;           // 128-byte column atoms along D
     static constexpr int ATOM = 128 * 128;         // bytes of one atom column of a 128-row tile
     static constexpr int TILE = NATOM * ATOM;      // a Q, K or V operand tile
+    // K and V tiles: 8-key groups of NATOM x 8 rows x 128 bytes, so that the
+    // groups lie a uniform stride apart (as the MMA descriptors need) and a
+    // block's 16 rows, both column atoms, are one 4 KB copy (head_dim 128).
+    // An SM pulls 33 B a clock in 4 KB copies but 23 in 2 KB ones
+    static constexpr int GROUP = NATOM * 1024;
     static constexpr int CODES = KT * D;           // a tile of E4M3 codes
-    // rings: together about 192 KB, so that the copies in flight cover the
-    // HBM latency (an SM's share of the bandwidth is ~24 B a clock)
-    static constexpr int NSK = FP8 ? 2 : (D == 128 ? 3 : 6), NSV = NSK;
+    // rings: what two query tiles leave of the shared memory, so that the
+    // copies in flight cover the HBM latency (an SM's share of the bandwidth
+    // is ~24 B a clock).  E4M3: operand tiles and a staging ring of codes
+    static constexpr int NSK = D == 128 ? (FP8 ? 2 : 3) : (FP8 ? 2 : 6);
+    static constexpr int NSV = D == 128 ? (FP8 ? 1 : 2) : (FP8 ? 2 : 6);
     static constexpr int NST = FP8 ? (D == 128 ? 4 : 12) : 0;
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = TILE;
+    static constexpr int OFF_K = 2 * TILE;
     static constexpr int OFF_V = OFF_K + NSK * TILE;
     static constexpr int OFF_C = OFF_V + NSV * TILE;
     static constexpr int OFF_ML = OFF_C + NST * CODES;     // [2][128] (m, l) of the two softmax warpgroups
     static constexpr int OFF_QEXP = OFF_ML + 2 * 128 * 8;
-    // E4M3: [4][128] query exponents, one byte each (items i .. i+3)
-    static constexpr int OFF_BAD = OFF_QEXP + (FP8 ? 4 * 128 : 0);
-    static constexpr int NBAD = 16;                        // ring of the tiles' bad-block masks
+    static constexpr int OFF_BAD = OFF_QEXP + (FP8 ? 4 * 128 : 0);  // E4M3: query exponents of 4 query tiles, a byte a row
+    static constexpr int NBAD = 16;                        // ring of the key tiles' bad-block masks
     static constexpr int OFF_BAR = OFF_BAD + NBAD * 4;
-    static constexpr int NBAR = 2 * NSK + 2 * NSV + 6 + 3 + 2 * NST;
+    static constexpr int NBAR = 2 * NSK + 2 * NSV + 6 + 5 + 2 * NST;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;    // TMEM address, share start
     static constexpr int USED = OFF_MISC + 64;
     static constexpr int SLACK = USED + 1024 <= 227 * 1024 ? 1024 : 0;  // else the base must be aligned (checked)
     static constexpr int SMEM = USED + SLACK;
     static constexpr int NWIDEN = FP8 ? 4 : 0;
-    static constexpr int W_LOAD = 8, W_MMA = 9, W_WIDEN = 12;  // warps 0-7: softmax; 10 and 11 only fill the warpgroup
+    // warps 0-7: softmax; 10 (E4M3: and 11): query tiles
+    static constexpr int W_LOAD = 8, W_MMA = 9, W_QUERY = 10, W_WIDEN = 12;
     static constexpr int NT = (12 + NWIDEN) * 32;
     static constexpr uint32_t COL_O = 2 * KT;
-    static constexpr uint32_t OP_ARRIVALS = FP8 ? NWIDEN * 32 : 1;  // arrivals that fill a Q, K or V tile
+    static constexpr uint32_t KV_ARRIVALS = FP8 ? NWIDEN * 32 : 1, Q_ARRIVALS = FP8 ? 64 : 1;  // that fill a tile
+    static constexpr float OPMUL = FP8 ? 256.f : 1.f;  // E4M3: K and V operands are 2^-8 of their value (widen4)
     // E4M3: P is kept 2^7 times larger, so that f16 holds weights down to
     // 2^-31 of the largest (and up to 2^(7 + 8) before the maximum moves)
     static constexpr float PBIAS = FP8 ? 7.f : 0.f;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(COL_O + 2 * D <= 512, "TMEM columns");
-    static_assert(NSK + 2 < NBAD && (NST == 0 || NST / 2 + NSK + 3 < NBAD), "bad-block ring");
+    static_assert(NSK + 3 < NBAD && NST / 2 + NSK + 3 < NBAD, "bad-block ring");
 };
 
 struct TreeWs {
-    float *o;    // [2 kMaxCtas][128][D] normalised partial outputs
-    float *lse;  // [2 kMaxCtas][128] log2-sum-exp
+    float *o;    // [2 kMaxCtas][256][D] normalised partial outputs
+    float *lse;  // [2 kMaxCtas][256] log2-sum-exp
     int4 *desc;  // [kMaxCtas]: (first q row, rows, kv head, pieces) of the cut segment that begins in CTA g; pieces 0: none
 };
 
-// A sequence of the batch.
+// A sequence of the batch: its metadata as loaded, and checked.
+struct Raw {
+    int q0, q1, P;
+};
 struct Seq {
-    int q0, T, P;        // first row, drafts (0 if its metadata is bad), prefix
-    int nmt, U;          // row tiles; line units of a segment
-    PA_DEVICE int units(int Hkv) const { return Hkv * nmt * U; }
+    int q0, T, P;          // first row, drafts (0 if its metadata is bad), prefix
+    int nt, npair, none;   // key tiles; segments of two and of one row tile per kv head
+    PA_DEVICE int units_head() const { return npair * (kSegCost + nt * kPair) + none * (kSegCost + nt * kOne); }
 };
 
+PA_DEVICE Raw load_raw(const TreeArgs &a, int b) {
+    b = min(b, a.B - 1);
+    return {a.cu_q[b], a.cu_q[b + 1], a.prefix_lens[b]};
+}
+
 template <class C>
-PA_DEVICE Seq load_seq(const TreeArgs &a, int b, bool flag) {
+PA_DEVICE Seq make_seq(const TreeArgs &a, const Raw &x, bool flag) {
     Seq s;
-    s.q0 = a.cu_q[b];
-    const int64_t q1 = a.cu_q[b + 1], T = q1 - s.q0;
-    s.P = a.prefix_lens[b];
-    s.T = (int)T;
-    if (s.q0 < 0 || T < 0 || T > a.max_q_len || q1 > a.total_q || s.P < 0 || s.P + T > (int64_t)a.max_blocks * 16) {
-        if (flag) flag_error(a.err, PA_DEVERR_BAD_LEN);
-        s.T = 0;
-        s.P = 0;
-    }
-    s.nmt = (s.T + C::QPOS - 1) / C::QPOS;
-    s.U = (s.P + s.T + C::KT - 1) / C::KT + kSegCost;
+    const int64_t T = (int64_t)x.q1 - x.q0;
+    const bool bad = x.q0 < 0 || T < 0 || T > a.max_q_len || x.q1 > a.total_q || x.P < 0 ||
+                     x.P + T > (int64_t)a.max_blocks * 16;
+    if (bad && flag) flag_error(a.err, PA_DEVERR_BAD_LEN);
+    s.q0 = x.q0;
+    s.T = bad ? 0 : (int)T;
+    s.P = bad ? 0 : x.P;
+    const int nmt = (s.T + C::QPOS - 1) / C::QPOS;
+    s.npair = nmt >> 1;
+    s.none = nmt & 1;
+    s.nt = (s.P + s.T + C::KT - 1) / C::KT;
     return s;
 }
 
 // Key tiles [j0, j1) of one segment.
 struct Item {
-    int b, kvh, q0, T, P, L;   // q0: first row of the row tile; T: drafts of the sequence
-    int nrows;                 // accumulator rows in use
+    int b, kvh, q0, T, P, L;   // q0: first row of the segment; T: drafts of the sequence
+    int r0, rt;                // first draft of the segment; its row tiles, 1 or 2
     int j0, j1, nt;            // nt: key tiles of the segment
-    int r0;                    // first draft of the row tile
+    int64_t tile0;             // line position of its first tile
+    PA_DEVICE int steps() const { return (j1 - j0) * rt; }
+    PA_DEVICE bool whole() const { return j0 == 0 && j1 == nt; }
 };
 
 // Walks a CTA's share of the line.
@@ -139,47 +162,59 @@ struct Walk {
     int64_t S;
     int b;
     Seq s;
+    Raw nxt;                 // sequence b + 1, loaded ahead
 
     PA_DEVICE void start(const TreeArgs &a, int64_t pos_, int64_t end_, int64_t S_, int b0, int64_t base0) {
         pos = pos_, end = end_, S = S_, b = b0, base = base0;
-        if (pos < end) s = load_seq<C>(a, b, false);
+        if (pos < end) {
+            s = make_seq<C>(a, load_raw(a, b), false);
+            nxt = load_raw(a, b + 1);
+        }
     }
     PA_DEVICE bool next(const TreeArgs &a, Item &it) {
+#pragma unroll 1
         while (pos < end) {
-            int off = (int)min(pos - base, (int64_t)INT32_MAX);
-            const int units = s.units(a.Hkv);
-            if (pos - base >= units) {
-                base += units;
-                s = load_seq<C>(a, ++b, false);
+            const int head = s.units_head();
+            const int64_t off64 = pos - base;
+            if (off64 >= (int64_t)head * a.Hkv) {
+                base += (int64_t)head * a.Hkv;
+                s = make_seq<C>(a, nxt, false);
+                nxt = load_raw(a, ++b + 1);
                 continue;
             }
-            const int seg = off / s.U, r = off - seg * s.U;
+            const unsigned off = (unsigned)off64;  // below 2^31: at most 128 kv heads x 3 segments x 2^24 units
+            it.kvh = off / (unsigned)head;
+            int r = off - it.kvh * head;           // unit within the kv head's segments, then within the segment
+            const int Up = kSegCost + s.nt * kPair;
+            int seg = r / Up;
+            it.rt = seg < s.npair ? 2 : 1;
+            seg = min(seg, s.npair);
+            r -= seg * Up;
+            const int wt = it.rt == 2 ? kPair : kOne, U = kSegCost + s.nt * wt;
+            const int stop = (int)min((int64_t)U, end - pos + r);
+            // the tiles whose first unit lies in the share
+            it.j0 = max(0, r - kSegCost + wt - 1) / wt;
+            it.j1 = max(0, stop - kSegCost + wt - 1) / wt;
             const int64_t seg0 = pos - r;
-            const int stop = (int)min((int64_t)s.U, end - seg0);
-            it.j0 = max(r - kSegCost, 0);
-            it.j1 = stop - kSegCost;
             pos = seg0 + stop;
             if (it.j1 <= it.j0) continue;
             it.b = b;
-            it.kvh = seg / s.nmt;
-            const int mt = seg - it.kvh * s.nmt;
-            it.r0 = mt * C::QPOS;
+            it.r0 = 2 * seg * C::QPOS;
             it.q0 = s.q0 + it.r0;
             it.T = s.T;
             it.P = s.P;
             it.L = s.P + s.T;
-            it.nrows = min(C::QPOS, s.T - it.r0) * C::G;
-            it.nt = s.U - kSegCost;
+            it.nt = s.nt;
+            it.tile0 = seg0 + kSegCost;
             return true;
         }
         return false;
     }
-    // pieces of the segment whose item ends at pos (it began in this share):
-    // the shares from the one that holds its first tile to the one that
-    // holds its last
+    // pieces of a segment: one for every share from the one that holds its
+    // first tile's first unit to the one that holds its last tile's
     PA_DEVICE int pieces(const Item &it) const {
-        const int64_t tile0 = pos - it.j1;  // line position of the segment's first tile
-        return (int)((tile0 + it.nt - 1) / S - tile0 / S) + 1;
+        const int64_t last = it.tile0 + (int64_t)(it.nt - 1) * (it.rt == 2 ? kPair : kOne);
+        return (int)(last / S - it.tile0 / S) + 1;
     }
 };
 
@@ -204,6 +239,65 @@ PA_DEVICE void tmem_st16_u(uint32_t taddr, const uint32_t (&r)[16]) {
         : "memory");
 }
 
+// True in one thread of the (converged) warp.  The tensor-core and TMA
+// instructions take their operands from uniform registers: behind this
+// predicate the compiler knows that one thread is active, behind lane == 0 it
+// wraps each of them in a loop over the active lanes' values.
+PA_DEVICE bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The 16 rows of a block (two groups of 8, from group `g`): columns, rows,
+// column atoms, groups.  No multicast.
+PA_DEVICE void tma_load_4d(void *dst_smem, const CUtensorMap *map, int g, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+        "[%4];" ::"r"(smem_addr(dst_smem)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(g), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane.
+PA_DEVICE void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Four E4M3 codes -> two f16x2 of 2^-8 their value: exponent and significand
+// moved up by 7 and the sign by 8, which leaves the exponent 8 below f16's
+// bias (subnormals included; a NaN code becomes 0x3f80).  Half of the steps
+// are multiplications (x 2^7), on the FMA pipe; the conversion instruction
+// shares its pipe with the exponentials.
+PA_DEVICE void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    uint32_t a, b;
+    asm("prmt.b32 %0, %1, 0, 0x4140;" : "=r"(a) : "r"(w));  // codes 0 and 1 as the low bytes of the halves
+    asm("prmt.b32 %0, %1, 0, 0x4342;" : "=r"(b) : "r"(w));
+    asm("mul.lo.u32 %0, %1, 128;" : "=r"(lo) : "r"(a));
+    asm("mad.lo.u32 %0, %1, 128, %0;" : "+r"(lo) : "r"(a & 0x00800080u));
+    asm("mul.lo.u32 %0, %1, 128;" : "=r"(hi) : "r"(b));
+    asm("mad.lo.u32 %0, %1, 128, %0;" : "+r"(hi) : "r"(b & 0x00800080u));
+}
+
+// Chunks 2u and 2u + 1 (8 f16 each) of a swizzled operand row.
+template <class C>
+PA_DEVICE void store_chunks(uint8_t *row, int u, int r, const uint32_t (&h)[8]) {
+#pragma unroll
+    for (int hc = 0; hc < 2; ++hc) {
+        const int ch = 2 * u + hc, at = ch / 8, cc = ch % 8;
+        *reinterpret_cast<uint4 *>(row + at * 1024 + ((cc ^ (r & 7)) * 16)) =
+            make_uint4(h[4 * hc], h[4 * hc + 1], h[4 * hc + 2], h[4 * hc + 3]);
+    }
+}
+
 PA_DEVICE bool not_finite(float x) { return !(fabsf(x) <= 3.4028235e38f); }
 
 // P.V multiplies the V rows of drafts that a row does not see by zero, and
@@ -214,6 +308,7 @@ PA_DEVICE bool not_finite(float x) { return !(fabsf(x) <= 3.4028235e38f); }
 template <class C>
 __device__ __noinline__ bool drafts_not_finite(const TreeArgs &a, const Item &it, int lane) {
     bool bad = false;
+#pragma unroll 1
     for (int t = it.P; t < it.L; ++t) {
         const int64_t blk = a.block_tables[(size_t)it.b * a.max_blocks + (t >> 4)];
         if (blk < 0 || blk >= a.num_blocks) continue;
@@ -235,6 +330,7 @@ __device__ __noinline__ void attend_row(const TreeArgs &a, const Item &it, int r
     const float sl2 = a.scale * kLog2e * (C::FP8 ? a.k_scale[it.kvh] : 1.f);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
     for (int t = it.j0 * C::KT; t < min(it.j1 * C::KT, it.L); ++t) {
         if (t >= it.P && !((bits >> (t - it.P)) & 1)) continue;
         const int64_t blk = a.block_tables[(size_t)it.b * a.max_blocks + (t >> 4)];
@@ -255,7 +351,7 @@ __device__ __noinline__ void attend_row(const TreeArgs &a, const Item &it, int r
 
 template <class C>
 __global__ void __launch_bounds__(C::NT, 1)
-    tree_kernel(const TreeArgs a, const TreeWs ws, const __grid_constant__ CUtensorMap tmK,
+    tree_kernel(const __grid_constant__ TreeArgs a, const TreeWs ws, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
     constexpr int D = C::D, G = C::G, KT = C::KT, NSK = C::NSK, NSV = C::NSV, NST = C::NST;
     extern __shared__ uint8_t smem_raw[];
@@ -267,7 +363,7 @@ __global__ void __launch_bounds__(C::NT, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *kfull = bars, *kempty = kfull + NSK, *vfull = kempty + NSK, *vempty = vfull + NSV;
     uint64_t *sfull = vempty + NSV, *pfull = sfull + 2, *odone = pfull + 2;
-    uint64_t *qfull = odone + 2, *qempty = qfull + 1, *mma_done = qempty + 1;
+    uint64_t *qfull = odone + 2, *qempty = qfull + 2, *mma_done = qempty + 2;
     uint64_t *cfull = mma_done + 1, *cempty = cfull + NST;  // E4M3: staging ring of codes
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     int *s_b0 = reinterpret_cast<int *>(smem + C::OFF_MISC + 4);
@@ -286,20 +382,20 @@ __global__ void __launch_bounds__(C::NT, 1)
     if (w == C::W_MMA) tmem_alloc(tmem_slot, 512);
     if (tid == C::W_LOAD * 32) {
         for (int i = 0; i < NSK; ++i) {
-            mbar_init(&kfull[i], C::OP_ARRIVALS);
+            mbar_init(&kfull[i], C::KV_ARRIVALS);
             mbar_init(&kempty[i], 1);
         }
         for (int i = 0; i < NSV; ++i) {
-            mbar_init(&vfull[i], C::OP_ARRIVALS);
+            mbar_init(&vfull[i], C::KV_ARRIVALS);
             mbar_init(&vempty[i], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sfull[s], 1);
             mbar_init(&pfull[s], 128);
             mbar_init(&odone[s], 1);
+            mbar_init(&qfull[s], C::Q_ARRIVALS);
+            mbar_init(&qempty[s], 1);
         }
-        mbar_init(qfull, C::OP_ARRIVALS);
-        mbar_init(qempty, 1);
         mbar_init(mma_done, 1);
         for (int i = 0; i < NST; ++i) {
             mbar_init(&cfull[i], 1);
@@ -314,7 +410,9 @@ __global__ void __launch_bounds__(C::NT, 1)
     {
         const int per = (a.B + C::NT - 1) / C::NT, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
         int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += load_seq<C>(a, b, blockIdx.x == 0).units(a.Hkv);
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b)
+            mine += (int64_t)make_seq<C>(a, load_raw(a, b), blockIdx.x == 0).units_head() * a.Hkv;
         int64_t x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -329,13 +427,13 @@ __global__ void __launch_bounds__(C::NT, 1)
             if (i < w) before += scan[i];
             total += scan[i];
         }
-        const int64_t S = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)1);
+        const int64_t S = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kPair);  // at least a tile's units
         const int64_t pos = (int64_t)blockIdx.x * S;
         if (pos >= before && pos < before + mine) {  // one thread at most
             int64_t at = before;
             int b = b0;
             for (;; ++b) {
-                const int u = load_seq<C>(a, b, false).units(a.Hkv);
+                const int64_t u = (int64_t)make_seq<C>(a, load_raw(a, b), false).units_head() * a.Hkv;
                 if (pos < at + u) break;
                 at += u;
             }
@@ -366,6 +464,8 @@ __global__ void __launch_bounds__(C::NT, 1)
         ok = ok && mbar_wait(bar, parity, deadline);
         return ok;
     };
+    // after a role's waits, which each lane makes for itself: its warp goes on together or not at all
+    auto agree = [&] { return ok = __all_sync(kFull, ok); };
     auto wait_all = [&](uint64_t *bar, uint32_t parity) {
         ok = ok && mbar_wait(bar, parity, deadline);
         ok = __all_sync(kFull, ok);
@@ -377,13 +477,7 @@ __global__ void __launch_bounds__(C::NT, 1)
         // items of the share; a window of 32 block-table entries in registers
         const int32_t *bt = nullptr;
         int win0 = 0, went = 0, nblk = 0;
-        auto open = [&](const Item &i) {
-            bt = a.block_tables + (size_t)i.b * a.max_blocks;
-            nblk = (i.L + 15) >> 4;
-            win0 = i.j0 * C::BPT;
-            went = bt[min(win0 + lane, nblk - 1)];
-        };
-        auto tile_row = [&](const Item &i, int j, int n) -> int64_t {  // lanes 0..7: cache row of the tile's block
+        auto tile_row = [&](const Item &i, int j, int n) {  // lanes 0..7: cache row of the tile's block
             const int jb = j * C::BPT;
             if (jb + C::BPT > win0 + 32) {
                 win0 = jb;
@@ -397,459 +491,555 @@ __global__ void __launch_bounds__(C::NT, 1)
                 if (bad) phys = 0;
             }
             if (lane == 0) badmask[n % C::NBAD] = m;
-            return ((int64_t)phys * a.Hkv + i.kvh) * 16;
+            return (phys * a.Hkv + i.kvh) * 16;
         };
         int kn = 0, vn = 0, cn = 0;  // tiles issued
-        auto fill = [&](int kv, int64_t row) {
+        auto fill = [&](int kv, int row) {
+            int rows[C::BPT];
+#pragma unroll
+            for (int i = 0; i < C::BPT; ++i) rows[i] = __shfl_sync(kFull, row, i);
             if constexpr (!C::FP8) {
                 const int ns = kv ? NSV : NSK, n = kv ? vn : kn, sl = n % ns;
-                if (n >= ns && !wait(kv ? &vempty[sl] : &kempty[sl], (n / ns - 1) & 1)) return false;
-                (kv ? vn : kn)++;
-                uint64_t *full = kv ? &vfull[sl] : &kfull[sl];
-                if (lane == 0) mbar_arrive_expect_tx(full, C::TILE);
-                __syncwarp();
-                if (lane < C::BPT) {
-                    uint8_t *dst = (kv ? sV : sK) + sl * C::TILE + lane * 16 * 128;
+                if (n >= ns) wait((kv ? vempty : kempty) + sl, (n / ns - 1) & 1);
+                if (!agree()) return false;
+                if (kv) ++vn; else ++kn;
+                uint64_t *full = (kv ? vfull : kfull) + sl;
+                uint8_t *dst = (kv ? sV : sK) + sl * C::TILE;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full, C::TILE);
+                    const CUtensorMap *map = kv ? &tmV : &tmK;
 #pragma unroll
-                    for (int at = 0; at < C::NATOM; ++at)
-                        tma_load_2d(dst + at * C::ATOM, kv ? &tmV : &tmK, at * 64, (int)row, full);
+                    for (int i = 0; i < C::BPT; ++i) tma_load_4d(dst + i * 2 * C::GROUP, map, rows[i] >> 3, full);
                 }
             } else {
                 const int sl = cn % NST;
-                if (cn >= NST && !wait(&cempty[sl], (cn / NST - 1) & 1)) return false;
+                if (cn >= NST) wait(&cempty[sl], (cn / NST - 1) & 1);
+                if (!agree()) return false;
                 ++cn;
-                if (lane == 0) mbar_arrive_expect_tx(&cfull[sl], C::CODES);
-                __syncwarp();
-                if (lane < C::BPT)
-                    tma_load_2d(sC + sl * C::CODES + lane * 16 * D, kv ? &tmV : &tmK, 0, (int)row, &cfull[sl]);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&cfull[sl], C::CODES);
+                    const CUtensorMap *map = kv ? &tmV : &tmK;
+#pragma unroll
+                    for (int i = 0; i < C::BPT; ++i)
+                        tma_load_2d(sC + sl * C::CODES + i * 16 * D, map, 0, rows[i], &cfull[sl]);
+                }
             }
             __syncwarp();
             return true;
         };
-        int n = 0;
-        int64_t vrow = -1;
-        bool go = walk.next(a, it);
-        while (go && ok) {
-            open(it);
+        int n = 0, vrow = 0;
+#pragma unroll 1
+        while (ok && walk.next(a, it)) {
+            bt = a.block_tables + (size_t)it.b * a.max_blocks;
+            nblk = (it.L + 15) >> 4;
+            win0 = it.j0 * C::BPT - 32;  // (refilled by the first tile)
+#pragma unroll 1
             for (int j = it.j0; j < it.j1 && ok; ++j, ++n) {
-                const int64_t row = tile_row(it, j, n);
-                if (!fill(0, row)) break;
-                if (n > 0 && !fill(1, vrow)) break;
+                const int row = tile_row(it, j, n);
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv)
+                    if ((kv == 0 || n > 0) && !fill(kv, kv ? vrow : row)) break;
                 vrow = row;
             }
-            go = ok && walk.next(a, it);
         }
         if (ok && n > 0) fill(1, vrow);
         if (!ok) {  // the last copy of every slot may be in flight: wait for it, with a short fresh budget
             const uint64_t dd = drain_deadline();
+            auto drain = [&](uint64_t *full, int ns, int issued) {
+#pragma unroll 1
+                for (int sl = 0; sl < ns; ++sl)
+                    if (issued > sl) mbar_wait(&full[sl], ((issued - 1 - sl) / ns) & 1, dd);
+            };
             if constexpr (!C::FP8) {
-                for (int sl = 0; sl < NSK; ++sl)
-                    if (kn > sl) mbar_wait(&kfull[sl], ((kn - 1 - sl) / NSK) & 1, dd);
-                for (int sl = 0; sl < NSV; ++sl)
-                    if (vn > sl) mbar_wait(&vfull[sl], ((vn - 1 - sl) / NSV) & 1, dd);
+                drain(kfull, NSK, kn);
+                drain(vfull, NSV, vn);
             } else {
-                for (int sl = 0; sl < NST; ++sl)
-                    if (cn > sl) mbar_wait(&cfull[sl], ((cn - 1 - sl) / NST) & 1, dd);
+                drain(cfull, NST, cn);
             }
             __syncwarp();
         }
     } else if (w == C::W_MMA) {
         constexpr uint32_t idS = idesc_f16kind_f32(128, KT, false, !C::FP8);
         constexpr uint32_t idO = idesc_f16kind_f32(128, D, true, !C::FP8);
-        int n = 0, item = 0;     // tile about to get its scores; items whose query tile was requested
-        bool q_flying = false;
-        auto load_q = [&](const Item &i) {  // bf16: one 3-D box per 64-column atom
-            if constexpr (!C::FP8) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(qfull, C::TILE);
-#pragma unroll
-                    for (int at = 0; at < C::NATOM; ++at)
-                        tma_load_3d(sQ + at * C::ATOM, &tmQ, at * 64, i.kvh * G, i.q0, qfull);
-                }
-                __syncwarp();
-                q_flying = true;
+        // counters instead of divisions by ring sizes: this warp's own
+        // instructions between two MMAs are time that the tensor pipe waits
+        struct Ring {
+            int slot;
+            uint32_t phase;
+            PA_DEVICE void next(int n) {
+                if (++slot == n) slot = 0, phase ^= 1;
             }
         };
-        auto scores = [&](int nn, bool last) {  // S(nn) = Q K^T, whose K tile and query tile have landed
-            if (lane == 0) {
+        // operand descriptors of the rings' first tiles; an address is 16 bytes a unit
+        const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024), dk = smem_desc_sw128(smem_addr(sK), 16, C::GROUP),
+                       dv = smem_desc_sw128(smem_addr(sV), 1024, C::GROUP);
+        int n = 0, kt = 0, qc = 0;   // steps, key tiles and query tiles before this one
+        Ring kr{0, 0}, vr{0, 0};     // this step's K tile; the V tile of the step whose P.V is still to issue:
+        int pn = -1, pbad = 0, pkv0 = 0, pL = 0;
+        bool pfirst = false, plast = false;  // the first of its accumulator; the last to read its V tile
+        auto scores = [&](int qslot, bool last_k, bool last_q) {  // S(n) = Q K^T
+            wait(&kfull[kr.slot], kr.phase);
+            if (n >= 2) wait(&odone[n & 1], ((n >> 1) - 1) & 1);  // P(n-2), in S(n)'s columns, has been used
+            if (!agree()) return;
+            if (elect_one()) {
                 tc_fence_after();
-                const uint32_t q0 = smem_addr(sQ), k0 = smem_addr(sK + nn % NSK * C::TILE);
+                const uint64_t a0 = dq + qslot * (C::TILE / 16), b0 = dk + kr.slot * (C::TILE / 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_bf16(tmem + (nn & 1) * KT, smem_desc_sw128(q0 + (kk / 4) * C::ATOM + (kk % 4) * 32, 16, 1024),
-                                smem_desc_sw128(k0 + (kk / 4) * C::ATOM + (kk % 4) * 32, 16, 1024), idS, kk > 0);
-                tc_commit(&sfull[nn & 1]);
-                tc_commit(&kempty[nn % NSK]);
-                if (last) tc_commit(qempty);
+                    tc_mma_bf16(tmem + (n & 1) * KT, a0 + ((kk / 4) * C::ATOM + (kk % 4) * 32) / 16,
+                                b0 + ((kk / 4) * 1024 + (kk % 4) * 32) / 16, idS, kk > 0);
+                tc_commit(&sfull[n & 1]);
+                if (last_k) tc_commit(&kempty[kr.slot]);
+                if (last_q) tc_commit(&qempty[qslot]);
             }
             __syncwarp();
         };
-        auto s_ready = [&](int nn) {  // its K tile has landed, its buffer is free (P(nn-2).V complete)
-            return wait(&kfull[nn % NSK], (nn / NSK) & 1) && (nn < 2 || wait(&odone[nn & 1], ((nn >> 1) - 1) & 1));
-        };
-        auto pv = [&](int nn, int kv0, int L, bool first) {  // O += P(nn) V(nn)
-            const int sl = nn % NSV;
-            if (!wait(&vfull[sl], (nn / NSV) & 1)) return;
+        auto pv = [&] {  // O += P(pn) V
+            wait(&vfull[vr.slot], vr.phase);
             if constexpr (!C::FP8) {  // rows past the end or of bad blocks: zero them before they meet P
-                const uint32_t bad = badmask[nn % C::NBAD];
-                if (kv0 + KT > L || bad) {
-                    uint8_t *vt = sV + sl * C::TILE;
+                const uint32_t bad = badmask[pbad % C::NBAD];
+                if (pkv0 + KT > pL || bad) {
+                    if (!agree()) return;
+                    uint8_t *vt = sV + vr.slot * C::TILE;
+#pragma unroll 1
                     for (int r = lane; r < KT; r += 32)
-                        if (kv0 + r >= L || ((bad >> (r >> 4)) & 1))
+                        if (pkv0 + r >= pL || ((bad >> (r >> 4)) & 1))
 #pragma unroll
-                            for (int at = 0; at < C::NATOM; ++at)
-#pragma unroll
-                                for (int cc = 0; cc < 8; ++cc)
-                                    *reinterpret_cast<uint4 *>(vt + at * C::ATOM + r * 128 + cc * 16) =
-                                        make_uint4(0, 0, 0, 0);
+                            for (int c = 0; c < C::NATOM * 8; ++c)
+                                *reinterpret_cast<uint4 *>(vt + (r >> 3) * C::GROUP + (r & 7) * 128 + (c / 8) * 1024 + (c % 8) * 16) =
+                                    make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
             }
-            if (!wait(&pfull[nn & 1], (nn >> 1) & 1)) return;
-            if (lane == 0) {
+            wait(&pfull[pn & 1], (pn >> 1) & 1);
+            if (!agree()) return;
+            if (elect_one()) {
                 tc_fence_after();
-                const uint32_t v0 = smem_addr(sV + sl * C::TILE);
+                const uint64_t b0 = dv + vr.slot * (C::TILE / 16);
+                const uint32_t o0 = tmem + C::COL_O + (pn & 1) * D, p0 = tmem + (pn & 1) * KT;
 #pragma unroll
                 for (int kk = 0; kk < KT / 16; ++kk)
-                    tc_mma_bf16_tmem_a(tmem + C::COL_O + (nn & 1) * D, tmem + (nn & 1) * KT + kk * 8,
-                                       smem_desc_sw128(v0 + kk * 16 * 128, C::ATOM, 1024), idO, !first || kk > 0);
-                tc_commit(&odone[nn & 1]);
-                tc_commit(&vempty[sl]);
+                    tc_mma_bf16_tmem_a(o0, p0 + kk * 8, b0 + kk * 2 * C::GROUP / 16, idO, !pfirst || kk > 0);
+                tc_commit(&odone[pn & 1]);
+                if (plast) tc_commit(&vempty[vr.slot]);
             }
             __syncwarp();
+            if (plast) vr.next(NSV);
         };
-        bool go = walk.next(a, it);
-        if (go) load_q(it);
-        while (go && ok) {
-            const Item cur = it;
-            const int cnt = cur.j1 - cur.j0;
-            bool more = false;
-            if (!wait(qfull, item & 1)) break;
-            q_flying = false;
-            ++item;
-            if (!s_ready(n)) break;
-            scores(n, cnt == 1);
-            for (int j = 0; j < cnt && ok; ++j) {
-                if (j + 1 < cnt) {
-                    if (!s_ready(n + 1)) break;
-                    scores(n + 1, j + 2 == cnt);
-                }
-                if (j + 2 >= cnt && (cnt == 1 || j + 2 == cnt)) {  // all scores issued: fetch the next query tile
-                    more = walk.next(a, it);
-                    if (!C::FP8 && more) {
-                        if (!wait(qempty, (item - 1) & 1)) break;
-                        load_q(it);
+        bool more = walk.next(a, it), was_pair = false;
+#pragma unroll 1
+        while (more && ok) {
+            const int steps = it.steps(), pair = it.rt - 1;
+#pragma unroll 1
+            for (int k = 0; k < steps && ok; ++k, ++n) {
+                const int qt = pair ? k & 1 : 0, qslot = (qc + qt) & 1;
+                // the scores first, so that the tensor pipe has them while
+                // P(n-1) is computed; but where a new query tile takes the
+                // place of one that the last scores read, P.V first
+                const bool pv_first = k == 0 && (pair || was_pair);
+#pragma unroll 1
+                for (int u = 0; u < 2 && ok; ++u) {
+                    if ((u == 0) == pv_first) {
+                        if (pn >= 0) pv();
+                    } else {
+                        if (k <= pair) wait(&qfull[qslot], ((qc + qt) >> 1) & 1);
+                        scores(qslot, !pair || (k & 1), k >= steps - 1 - pair);
                     }
                 }
-                pv(n, (cur.j0 + j) * KT, cur.L, j < 2);
-                ++n;
+                pn = n;
+                pkv0 = (it.j0 + (pair ? k >> 1 : k)) * KT;
+                pL = it.L;
+                pfirst = k < 2;
+                pbad = kt;
+                plast = !pair || (k & 1);
+                if (plast) {
+                    kr.next(NSK);
+                    ++kt;
+                }
             }
-            go = more;
+            qc += it.rt;
+            was_pair = pair;
+            more = ok && walk.next(a, it);
         }
-        // every MMA of this CTA has completed before TMEM is released, and
-        // the query copy has landed
-        if (lane == 0) tc_commit(mma_done);
+        if (ok && pn >= 0) pv();
+        // every MMA of this CTA has completed before TMEM is released
+        if (elect_one()) tc_commit(mma_done);
         __syncwarp();
-        if (!ok && q_flying) mbar_wait(qfull, item & 1, drain_deadline());
         const bool done = mbar_wait(mma_done, 0, ok ? deadline : drain_deadline());
         ok = __all_sync(kFull, ok && done);
-    } else if (w >= C::W_WIDEN) {
-      if constexpr (C::FP8) {
-        // ---- E4M3: thread ct widens key row ct of each staged tile into its
-        // f16 operand tile, and scales query row ct
-        const int ct = tid - C::W_WIDEN * 32;
-        int kn = 0, vn = 0, cn = 0, item = 0;
-        auto widen = [&](int kv, int kv0, int L, int n) {
-            const int ns = kv ? NSV : NSK, m = kv ? vn : kn, sl = m % ns, cs = cn % NST;
-            if (!wait(&cfull[cs], (cn / NST) & 1)) return false;
-            if (m >= ns && !wait(kv ? &vempty[sl] : &kempty[sl], (m / ns - 1) & 1)) return false;
-            (kv ? vn : kn)++;
-            ++cn;
-            uint8_t *tile = (kv ? sV : sK) + sl * C::TILE;
-            const uint8_t *codes = sC + cs * C::CODES + ct * D;
-            const bool live = kv0 + ct < L && !((badmask[n % C::NBAD] >> (ct >> 4)) & 1);
-            uint4 src[D / 16];
+    } else if (w >= C::W_QUERY && w < C::W_WIDEN) {
+        // ---- query tiles, two slots in turn.  bf16: warp 10, one 3-D box per
+        // 64-column atom.  E4M3: warps 10 and 11, f16(q 2^e) with e per row
+        // such that its largest magnitude lies in [2^14, 2^15) (exact for
+        // components within 2^-28 of it)
+        int qc = 0;
+#pragma unroll 1
+        while (ok && (C::FP8 || w == C::W_QUERY) && walk.next(a, it)) {
+#pragma unroll 1
+            for (int qt = 0; qt < it.rt && ok; ++qt, ++qc) {
+                const int sl = qc & 1;
+                if (qc >= 2) wait(&qempty[sl], ((qc >> 1) - 1) & 1);
+                if (!agree()) break;
+                const int q0 = it.q0 + qt * C::QPOS;
+                uint8_t *tile = sQ + sl * C::TILE;
+                if constexpr (!C::FP8) {
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&qfull[sl], C::TILE);
 #pragma unroll
-            for (int u = 0; u < D / 16; ++u) {  // the codes' rows are swizzled too: conflict-free columns
-                const int ch = D == 128 ? (u ^ (ct & 7)) : (u ^ ((ct >> 1) & 3));
-                src[u] = live ? *reinterpret_cast<const uint4 *>(codes + 16 * ch) : make_uint4(0, 0, 0, 0);
-            }
+                        for (int at = 0; at < C::NATOM; ++at)
+                            tma_load_3d(tile + at * C::ATOM, &tmQ, at * 64, it.kvh * G, q0, &qfull[sl]);
+                    }
+                    __syncwarp();
+                } else {
+                    // a row is LPR lanes of 8 dims; the warp's rows RPW apart
+                    constexpr int LPR = D / 8, RPW = 32 / LPR;
+                    const int nrows = min(C::QPOS, it.T - it.r0 - qt * C::QPOS) * G;
+                    const int ch = lane % LPR, at = ch / 8, cc = ch % 8;
+#pragma unroll 1
+                    for (int rb = (w - C::W_QUERY) * 64 + lane / LPR; rb < (w - C::W_QUERY + 1) * 64; rb += 8 * RPW) {
+                    uint4 v[8];  // 8 rows' loads in flight
 #pragma unroll
-            for (int u = 0; u < D / 16; ++u) {
-                const uint32_t wd[4] = {src[u].x, src[u].y, src[u].z, src[u].w};
-                uint32_t h[8];
+                    for (int u = 0; u < 8; ++u) {
+                        const int r = rb + u * RPW;
+                        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
+                                                   ((size_t)(q0 + r / G) * a.Hq + (size_t)it.kvh * G + r % G) * D + ch * 8;
+                        v[u] = r < nrows ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    h[2 * e] = e4m3x2_to_h2(wd[e]);
-                    h[2 * e + 1] = e4m3x2_to_h2(wd[e] >> 16);
+                    for (int u = 0; u < 8; ++u) {
+                        const int r = rb + u * RPW;
+                        const uint32_t wd[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                        float2 f[4];
+                        float amax = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f[e] = bf16x2_to_float2(wd[e]);
+                            amax = fmax3(amax, fabsf(f[e].x), fabsf(f[e].y));
+                        }
+#pragma unroll
+                        for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+                        int ex = 0;
+                        if (amax > 0.f) ex = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xff) - 127), -100), 100);
+                        const float qs = __uint_as_float((uint32_t)(127 + ex) << 23);
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __half2 hh = __floats2half2_rn(f[e].x * qs, f[e].y * qs);
+                            h[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                        }
+                        *reinterpret_cast<uint4 *>(tile + at * C::ATOM + r * 128 + ((cc ^ (r & 7)) * 16)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                        if (ch == 0) qexp[(qc & 3) * 128 + r] = (int8_t)ex;
+                    }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&qfull[sl]);
                 }
-#pragma unroll
-                for (int hc = 0; hc < 2; ++hc) {
-                    const int ch = 2 * u + hc, at = ch / 8, cc = ch % 8;
-                    *reinterpret_cast<uint4 *>(tile + at * C::ATOM + ct * 128 + ((cc ^ (ct & 7)) * 16)) =
-                        make_uint4(h[4 * hc], h[4 * hc + 1], h[4 * hc + 2], h[4 * hc + 3]);
-                }
-            }
-            mbar_arrive(&cempty[cs]);
-            fence_proxy_async_smem();
-            mbar_arrive(kv ? &vfull[sl] : &kfull[sl]);
-            return true;
-        };
-        auto query = [&](const Item &i) {  // f16(q 2^e), e per row: its largest magnitude in [2^14, 2^15)
-            const bool live = ct < i.nrows;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                static_cast<const __nv_bfloat16 *>(a.q) + ((size_t)(i.q0 + ct / G) * a.Hq + (size_t)i.kvh * G + ct % G) * D);
-            uint4 v[D / 8];
-            float amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-                v[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
-                const uint32_t wd[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = bf16x2_to_float2(wd[e]);
-                    amax = fmax3(amax, fabsf(f.x), fabsf(f.y));
-                }
-            }
-            int ex = 0;
-            if (amax > 0.f) ex = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xff) - 127), -100), 100);
-            const float qs = __uint_as_float((uint32_t)(127 + ex) << 23);
-            if (item > 0 && !wait(qempty, (item - 1) & 1)) return false;
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-                const uint32_t wd[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = bf16x2_to_float2(wd[e]);
-                    const __half2 hh = __floats2half2_rn(f.x * qs, f.y * qs);
-                    h[e] = *reinterpret_cast<const uint32_t *>(&hh);
-                }
-                const int at = k / 8, cc = k % 8;
-                *reinterpret_cast<uint4 *>(sQ + at * C::ATOM + ct * 128 + ((cc ^ (ct & 7)) * 16)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            qexp[(item & 3) * 128 + ct] = (int8_t)ex;
-            ++item;
-            fence_proxy_async_smem();
-            mbar_arrive(qfull);
-            return true;
-        };
-        // K tile n+1 before V tile n, as the loader; an item's query tile
-        // before the first V that follows its first K
-        int n = 0, vkv0 = 0, vL = 0;
-        while (ok && walk.next(a, it)) {
-            for (int j = it.j0; j < it.j1 && ok; ++j, ++n) {
-                if (!widen(0, j * KT, it.L, n)) break;
-                if (n > 0 && !widen(1, vkv0, vL, n - 1)) break;
-                if (j == it.j0 && !query(it)) break;
-                vkv0 = j * KT;
-                vL = it.L;
             }
         }
-        if (ok && n > 0) widen(1, vkv0, vL, n - 1);
-      }
-    } else if (w < 8) {
-        // ---- softmax: warpgroup g takes the tiles n with n % 2 == g; thread
-        // = row r of the row tile
+        if (!C::FP8 && w == C::W_QUERY) {  // the copies have landed before the CTA may exit
+            const uint64_t dd = ok ? deadline : drain_deadline();
+            for (int sl = 0; sl < 2; ++sl)
+                if (qc > sl && !mbar_wait(&qfull[sl], ((qc - 1 - sl) >> 1) & 1, dd)) ok = false;
+            __syncwarp();
+        }
+    } else if (w >= C::W_WIDEN) {
+        if constexpr (C::FP8) {
+            // ---- E4M3: thread ct widens key row ct of each staged tile into its
+            // f16 operand tile
+            const int ct = tid - C::W_WIDEN * 32;
+            int kn = 0, vn = 0, cn = 0, n = 0, vkv0 = 0, vL = 0;
+            auto widen = [&](int kv, int kv0, int L, int nn) {
+                const int ns = kv ? NSV : NSK, m = kv ? vn : kn, sl = m % ns, cs = cn % NST;
+                if (!wait(&cfull[cs], (cn / NST) & 1)) return false;
+                if (m >= ns && !wait((kv ? vempty : kempty) + sl, (m / ns - 1) & 1)) return false;
+                if (kv) ++vn; else ++kn;
+                ++cn;
+                uint8_t *row = (kv ? sV : sK) + sl * C::TILE + (ct >> 3) * C::GROUP + (ct & 7) * 128;
+                const uint8_t *codes = sC + cs * C::CODES + ct * D;
+                const bool live = kv0 + ct < L && !((badmask[nn % C::NBAD] >> (ct >> 4)) & 1);
+                uint4 src[D / 16];
+#pragma unroll
+                for (int u = 0; u < D / 16; ++u) {  // the codes' rows are swizzled too: conflict-free columns
+                    const int ch = D == 128 ? (u ^ (ct & 7)) : (u ^ ((ct >> 1) & 3));
+                    src[u] = live ? *reinterpret_cast<const uint4 *>(codes + 16 * ch) : make_uint4(0, 0, 0, 0);
+                }
+                mbar_arrive(&cempty[cs]);
+                uint32_t nan = 0;
+#pragma unroll
+                for (int u = 0; u < D / 16; ++u) {
+                    const uint32_t wd[4] = {src[u].x, src[u].y, src[u].z, src[u].w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        widen4(wd[e], h[2 * e], h[2 * e + 1]);
+                        nan |= (wd[e] & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a byte: its code is a NaN
+                    }
+                    store_chunks<C>(row, u, ct, h);
+                }
+                if (nan & 0x80808080u) {  // a NaN has no place in the scaled range: write it
+#pragma unroll 1
+                    for (int d = 0; d < D; ++d) {
+                        const int at = d / 64, cc = d % 64 / 8;
+                        uint16_t *x = reinterpret_cast<uint16_t *>(row + at * 1024 + ((cc ^ (ct & 7)) * 16)) + d % 8;
+                        if ((*x & 0x7fff) == 0x3f80) *x = 0x7fff;
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive((kv ? vfull : kfull) + sl);
+                return true;
+            };
+            bool more = true;
+#pragma unroll 1
+            while (ok && more) {  // K tile n+1 before V tile n, as the loader; at the end the last V tile alone
+                more = walk.next(a, it);
+                const int cnt = more ? it.j1 - it.j0 : 1;
+#pragma unroll 1
+                for (int j = 0; j < cnt && ok; ++j) {
+                    const int kv0 = (it.j0 + j) * KT;
+#pragma unroll 1
+                    for (int kv = more ? 0 : 1; kv < 2; ++kv)
+                        if ((kv == 0 || n > 0) && !widen(kv, kv ? vkv0 : kv0, kv ? vL : it.L, kv ? n - 1 : n)) break;
+                    vkv0 = kv0;
+                    vL = it.L;
+                    ++n;
+                }
+            }
+        }
+    } else {
+        // ---- softmax: warpgroup g takes the steps n with n % 2 == g; thread
+        // = row r of the step's row tile
         const int g = w >> 2, r = (w & 3) * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)((w & 3) * 32) << 16);
-        const uint32_t scol = g * KT, ocol = C::COL_O + g * D;
-        int n = 0, item = 0;
+        const uint32_t scol = lane_base + g * KT, ocol = lane_base + C::COL_O + g * D;
+        int n = 0, kt = 0, qc = 0;
         int4 desc = make_int4(0, 0, 0, 0);
+#pragma unroll 1
         while (walk.next(a, it)) {
-            const int cnt = it.j1 - it.j0;
-            const bool warp_live = (w & 3) * 32 < it.nrows, row_live = r < it.nrows;
-            uint64_t bits = 0;
-            if (row_live) {
-                bits = a.mask[it.q0 + r / G];
-                if (it.T < 64) bits &= (1ull << it.T) - 1;
-            }
-            float sl2 = a.scale * kLog2e * (C::FP8 ? a.k_scale[it.kvh] : 1.f);
-            const float vs = C::FP8 ? a.v_scale[it.kvh] : 1.f;
+            const int steps = it.steps(), pair = it.rt - 1;
+            const int k0 = (n ^ g) & 1, qt = pair & k0;       // first step of this warpgroup, its row tile
+            const int nrows = min(C::QPOS, it.T - it.r0 - qt * C::QPOS) * G;
+            const bool warp_live = (w & 3) * 32 < nrows, row_live = r < nrows;
+            const int64_t qrow = it.q0 + qt * C::QPOS + r / G;
+            const uint64_t bits = row_live ? a.mask[qrow] : 0;
+            float sl2 = a.scale * kLog2e * C::OPMUL * (C::FP8 ? a.k_scale[it.kvh] : 1.f);
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
-            bool have = false;
-            for (int j = (n ^ g) & 1; j < cnt; j += 2) {
-                const int nn = n + j, kv0 = (it.j0 + j) * KT;
+#pragma unroll 1
+            for (int k = k0; k < steps; k += 2) {
+                const int nn = n + k, kv0 = (it.j0 + (pair ? k >> 1 : k)) * KT;
                 const bool landed = wait_all(&sfull[g], (nn >> 1) & 1);
                 if (landed && warp_live) {
                     tc_fence_after();
-                    if (C::FP8 && !have) sl2 *= __uint_as_float((uint32_t)(127 - qexp[(item & 3) * 128 + r]) << 23);
+                    if (C::FP8 && k == k0)
+                        sl2 *= __uint_as_float((uint32_t)(127 - qexp[((qc + qt) & 3) * 128 + r]) << 23);
                     // the keys this row may see, where the tile is not all prefix
-                    const uint32_t bad = badmask[nn % C::NBAD];
+                    const uint32_t bad = badmask[(kt + (pair ? k >> 1 : k)) % C::NBAD];
                     const bool masked = kv0 + KT > it.P || bad;
-                    auto visible = [&](int q) -> uint32_t {  // keys kv0 + 32 q + [0, 32)
-                        const int rel = kv0 + 32 * q - it.P;  // draft of the first one
-                        uint32_t v = rel <= -32  ? kFull
+                    // scores of keys kv0 + CW h + [0, CW), requested, and masked once they are there
+                    constexpr int CW = C::FP8 ? 16 : 32;  // (an E4M3 CTA's threads have fewer registers)
+                    auto request = [&](int h, float (&sv)[CW]) {
+                        if constexpr (CW == 32) tmem_ld32(scol + CW * h, sv);
+                        else tmem_ld16(scol + CW * h, sv);
+                    };
+                    auto mask = [&](int h, float (&sv)[CW]) {
+                        const int rel = kv0 + CW * h - it.P;  // draft of the first key
+                        const uint64_t seen = it.T < 64 ? bits & ((1ull << it.T) - 1) : bits;
+                        uint32_t v = rel <= -CW  ? kFull
                                      : rel >= 64 ? 0u
-                                     : rel < 0   ? (uint32_t)((bits << -rel) | ((1ull << -rel) - 1))
-                                                 : (uint32_t)(bits >> rel);
-                        if ((bad >> (2 * q)) & 1) v &= 0xffff0000u;
-                        if ((bad >> (2 * q + 1)) & 1) v &= 0x0000ffffu;
-                        return v;
+                                     : rel < 0   ? (uint32_t)((seen << -rel) | ((1ull << -rel) - 1))
+                                                 : (uint32_t)(seen >> rel);
+                        if ((bad >> (CW / 16 * h)) & 1) v &= 0xffff0000u;
+                        if (CW == 32 && ((bad >> (2 * h + 1)) & 1)) v &= 0x0000ffffu;
+#pragma unroll
+                        for (int e = 0; e < CW; ++e) sv[e] = v & (1u << e) ? sv[e] : -INFINITY;
                     };
-                    constexpr int NH = 4, HC = KT / NH;  // the scores are read twice, HC in registers at a time
-                    float sv[HC];
-                    auto load = [&](int h) {
+                    auto largest = [&](const float (&sv)[CW], float mx) {
 #pragma unroll
-                        for (int q = 0; q < HC / 32; ++q) {
-                            float t32[32];
-                            tmem_ld32(lane_base + scol + h * HC + 32 * q, t32);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) sv[32 * q + e] = t32[e];
-                        }
-                        tmem_wait_ld();
-                        if (masked) {
-#pragma unroll
-                            for (int q = 0; q < HC / 32; ++q) {
-                                const uint32_t v = visible(h * (HC / 32) + q);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) sv[32 * q + e] = (v >> e) & 1 ? sv[32 * q + e] : -INFINITY;
-                            }
-                        }
+                        for (int e = 0; e < CW; e += 2) mx = fmax3(mx, sv[e], sv[e + 1]);
+                        return mx;
                     };
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        load(h);
-#pragma unroll
-                        for (int e = 0; e < HC; e += 2) mx = fmax3(mx, sv[e], sv[e + 1]);
+                    // the segment's first step takes its maximum beforehand;
+                    // later ones exponentiate against the maximum so far and
+                    // do it again in the rare case that a score exceeds it by
+                    // more than the threshold (P is held in registers, the
+                    // scores stay, until then)
+                    if (k == k0) {
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int h = 0; h < KT / CW; ++h) {
+                            float sv[CW];
+                            request(h, sv);
+                            tmem_wait_ld();
+                            if (masked) mask(h, sv);
+                            mx = largest(sv, mx);
+                        }
+                        m = mx * sl2;  // (the scale is positive)
                     }
-                    const float mt = mx * sl2;  // (the scale is positive)
-                    const bool rescale = mt > m + kRescaleThreshold;
-                    float alpha = 1.f;
-                    if (rescale) {
-                        alpha = ex2(m - mt);  // m = -inf: 0
-                        m = mt;
-                        l2 = make_float2(l2.x * alpha, l2.y * alpha);
-                    }
-                    const float nb = (m == -INFINITY ? 0.f : -m) + C::PBIAS;
-                    const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(nb, nb);
+                    uint32_t pk[KT / 2];
+                    float2 sum;
+#pragma unroll 1
+                    for (;;) {
+                        const float nb = (m == -INFINITY ? 0.f : -m) + C::PBIAS;
+                        const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(nb, nb);
+                        float mx = -INFINITY;
+                        sum = make_float2(0.f, 0.f);
+                        float sv[2][CW];  // two buffers: the next load is in flight during the arithmetic
+                        request(0, sv[0]);
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        if (NH > 1) load(h);
+                        for (int h = 0; h < KT / CW; ++h) {
+                            tmem_wait_ld();
+                            if (h + 1 < KT / CW) request(h + 1, sv[(h + 1) & 1]);
+                            float(&x)[CW] = sv[h & 1];
+                            if (masked) mask(h, x);
+                            mx = largest(x, mx);
 #pragma unroll
-                        for (int q = 0; q < HC / 32; ++q) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 x = ffma2(make_float2(sv[32 * q + e], sv[32 * q + e + 1]), sc2, nb2);
-                                const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                                l2 = fadd2(l2, p);
+                            for (int e = 0; e < CW; e += 2) {
+                                const float2 y = ffma2(make_float2(x[e], x[e + 1]), sc2, nb2);
+                                const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                                sum = fadd2(sum, p);
                                 if constexpr (C::FP8) {
                                     const __half2 hh = __floats2half2_rn(p.x, p.y);
-                                    pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hh);
+                                    pk[CW / 2 * h + e / 2] = *reinterpret_cast<const uint32_t *>(&hh);
                                 } else {
                                     const __nv_bfloat162 bb = __floats2bfloat162_rn(p.x, p.y);
-                                    pk[e / 2] = *reinterpret_cast<const uint32_t *>(&bb);
+                                    pk[CW / 2 * h + e / 2] = *reinterpret_cast<const uint32_t *>(&bb);
                                 }
                             }
-                            // P over score columns that this thread has read
-                            tmem_st16_u(lane_base + scol + 16 * (h * (HC / 32) + q), pk);
+                        }
+                        const float mt = mx * sl2;
+                        const bool rescale = mt > m + kRescaleThreshold;
+                        if (!__any_sync(kFull, rescale)) break;
+                        // O holds P.V up to this stream's previous step, complete
+                        // (this step's scores were issued after it)
+                        const float alpha = rescale ? ex2(m - mt) : 1.f;  // m = -inf: 0
+                        if (rescale) m = mt;
+                        l2 = make_float2(l2.x * alpha, l2.y * alpha);
+                        if (k > k0) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 16; ++q) {
+                                float o[16];
+                                tmem_ld16(ocol + 16 * q, o);
+                                tmem_wait_ld();
+                                uint32_t ou[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * alpha);
+                                tmem_st16_u(ocol + 16 * q, ou);
+                            }
                         }
                     }
-                    // O holds P.V up to this warpgroup's previous tile, complete
-                    // (this tile's scores were issued after it)
-                    if (have && __any_sync(kFull, rescale)) {
-#pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
-                            float o[32];
-                            tmem_ld32(lane_base + ocol + 32 * q, o);
-                            tmem_wait_ld();
+                    l2 = fadd2(l2, sum);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tmem_st32(lane_base + ocol + 32 * q, o);
-                        }
+                    for (int h = 0; h < 2; ++h) {  // P over the scores, all of which this thread has read
+                        uint32_t half[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) half[e] = pk[32 * h + e];
+                        tmem_st32_u(scol + 32 * h, half);
                     }
                     tmem_wait_st();
                     tc_fence_before();
-                    have = true;
                 }
                 mbar_arrive(&pfull[g]);
             }
-            // ---- join the two accumulators: warpgroup g writes columns
-            // [g D/2, (g+1) D/2) of every row
-            ml[g * 128 + r] = make_float2(m, l2.x + l2.y);
-            named_bar_sync(kEpiBar, 256);
-            const float2 ml0 = ml[r], ml1 = ml[128 + r];
-            const int last = n + cnt - 1;  // its stream's last tile; the other stream's is last - 1
-            bool landed = wait_all(&odone[last & 1], (last >> 1) & 1);
-            if (cnt > 1) landed = wait_all(&odone[(last - 1) & 1], ((last - 1) >> 1) & 1);
-            const bool one = cnt == 1;  // a single tile: one accumulator
-            const float M = fmaxf(ml0.x, ml1.x);
-            const float f0 = ml0.x == -INFINITY ? 0.f : ex2(ml0.x - M), f1 = ml1.x == -INFINITY ? 0.f : ex2(ml1.x - M);
-            const float l = ml0.y * f0 + ml1.y * f1;
-            const float inv = (l > 0.f ? 1.f / l : l == l ? 0.f : l) * vs;
-            const bool whole = it.j0 == 0 && it.j1 == it.nt;
-            const size_t grow = ((size_t)(it.q0 + r / G) * a.Hq + (size_t)it.kvh * G + r % G);
-            const int slot = blockIdx.x * 2 + (it.j0 == 0 ? 1 : 0);
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + grow * D + g * (D / 2);
-            float *wo = ws.o + ((size_t)slot * 128 + r) * D + g * (D / 2);
+            // ---- epilogue: two row tiles: this warpgroup's rows, all columns;
+            // one: the accumulators joined, columns [g D/2, (g+1) D/2)
+            const int last = n + steps - 1;  // the last step; the other stream's is last - 1
+            float M = m, l = l2.x + l2.y, f0 = 1.f, f1 = 0.f;
+            bool landed = true;
+            if (!pair) {
+                ml[g * 128 + r] = make_float2(m, l);
+                named_bar_sync(kEpiBar, 256);
+                const float2 ml0 = ml[r], ml1 = ml[128 + r];
+                M = fmaxf(ml0.x, ml1.x);
+                f0 = ml0.x == -INFINITY ? 0.f : ex2(ml0.x - M);
+                f1 = ml1.x == -INFINITY ? 0.f : ex2(ml1.x - M);
+                l = ml0.y * f0 + ml1.y * f1;
+            }
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+                const int nn = last - u;
+                if ((pair && (nn & 1) != g) || (u == 1 && steps == 1)) continue;
+                landed = wait_all(&odone[nn & 1], (nn >> 1) & 1);
+            }
+            const float inv = (l > 0.f ? 1.f / l : l == l ? 0.f : l) * C::OPMUL * (C::FP8 ? a.v_scale[it.kvh] : 1.f);
+            // accumulator A (first, in a pair this stream's), and B where both streams ran
+            const bool both = !pair && steps > 1;
+            const uint32_t colA = lane_base + C::COL_O + (pair ? g * D : both ? 0 : (last & 1) * D);
+            const uint32_t colB = both ? colA + D : colA;
+            const bool dead = l == 0.f;  // sees nothing: zeros
+            const float wA = (pair ? 1.f : both || !(last & 1) ? f0 : f1) * inv, wB = both ? f1 * inv : 0.f;
+            const int c0 = pair ? 0 : g * (D / 2), c1 = pair ? D : c0 + D / 2;
+            const bool whole = it.whole();
+            const int slot = blockIdx.x * 2 + (it.j0 == 0 ? 1 : 0), srow = slot * 256 + qt * 128;
+            auto out_row = [&](int rr) {
+                return static_cast<__nv_bfloat16 *>(a.out) +
+                       ((it.q0 + qt * C::QPOS + rr / G) * (int64_t)a.Hq + it.kvh * G + rr % G) * D;
+            };
             if (landed && warp_live) {
                 tc_fence_after();
-                bool odd = false;
+                __nv_bfloat16 *dst = out_row(r);
+                float *wo = ws.o + (size_t)(srow + r) * D;
+                float zero = 0.f;  // turns NaN where an output is not finite
 #pragma unroll 1
-                for (int q = 0; q < D / 64; ++q) {
-                    float o[32], o1[32];
-                    const uint32_t col = lane_base + C::COL_O + g * (D / 2) + 32 * q;
-                    tmem_ld32(col + (one ? (last & 1) * D : 0), o);
-                    if (!one) tmem_ld32(col + D, o1);
+                for (int c = c0; c < c1; c += 16) {
+                    float o[16], ob[16];
+                    tmem_ld16(colA + c, o);
+                    tmem_ld16(colB + c, ob);
                     tmem_wait_ld();
-                    const float w0 = (one ? ((last & 1) ? f1 : f0) : f0) * inv, w1 = f1 * inv;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        o[e] = l == 0.f ? 0.f : one ? o[e] * w0 : fmaf(o1[e], w1, o[e] * w0);
-                        odd |= not_finite(o[e]);
+                    for (int e = 0; e < 16; ++e) {
+                        o[e] = fmaf(ob[e], wB, o[e] * wA);
+                        o[e] = dead ? 0.f : o[e];
+                        zero = fmaf(o[e], 0.f, zero);
                     }
                     if (!row_live) continue;
                     if (whole) {
+                        uint32_t wd[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t wd[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const __nv_bfloat162 bb = __floats2bfloat162_rn(o[e + 2 * u], o[e + 2 * u + 1]);
-                                wd[u] = *reinterpret_cast<const uint32_t *>(&bb);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + 32 * q + e) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+                        for (int u = 0; u < 8; ++u) {
+                            const __nv_bfloat162 bb = __floats2bfloat162_rn(o[2 * u], o[2 * u + 1]);
+                            wd[u] = *reinterpret_cast<const uint32_t *>(&bb);
                         }
+                        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+                        *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(wd[4], wd[5], wd[6], wd[7]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(wo + 32 * q + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(wo + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
-                if (!whole && row_live && g == 0)
-                    ws.lse[slot * 128 + r] = l > 0.f ? M + lg2(l) - C::PBIAS : l == l ? -INFINITY : l;
+                if (!whole && row_live && (pair || g == 0))
+                    ws.lse[srow + r] = l > 0.f ? M + lg2(l) - C::PBIAS : l == l ? -INFINITY : l;
                 // rows that an unseen draft's V spoilt
-                uint32_t todo = __ballot_sync(kFull, odd && row_live && l > 0.f && l <= 3.4028235e38f);
-                if (todo && it.j1 * KT > it.P && drafts_not_finite<C>(a, it, lane)) {
+                uint32_t todo = __ballot_sync(kFull, zero != 0.f && row_live && l > 0.f && l <= 3.4028235e38f);
+                const Item copy = it;  // (what a call takes by reference lives in local memory: not the loop's own)
+                if (todo && it.j1 * KT > it.P && drafts_not_finite<C>(a, copy, lane)) {
+#pragma unroll 1
                     while (todo) {
-                        const int rl = __ffs(todo) - 1;
+                        const int rl = __ffs(todo) - 1, rr = (w & 3) * 32 + rl;
                         todo &= todo - 1;
-                        const int rr = (w & 3) * 32 + rl;
                         float acc[D / 32];
-                        attend_row<C>(a, it, rr, __shfl_sync(kFull, bits, rl), __shfl_sync(kFull, M, rl) - C::PBIAS, lane, acc);
-                        const float iv = __shfl_sync(kFull, inv, rl);
-                        if ((lane * (D / 32)) / (D / 2) == g) {
-                            const size_t gr = (size_t)(it.q0 + rr / G) * a.Hq + (size_t)it.kvh * G + rr % G;
+                        attend_row<C>(a, copy, qt * 128 + rr, __shfl_sync(kFull, bits, rl),
+                                      __shfl_sync(kFull, M, rl) - C::PBIAS, lane, acc);
+                        const float iv = __shfl_sync(kFull, inv, rl) * (1.f / C::OPMUL);
 #pragma unroll
-                            for (int e = 0; e < D / 32; ++e) {
-                                const int d = lane * (D / 32) + e;
-                                if (whole) static_cast<__nv_bfloat16 *>(a.out)[gr * D + d] = __float2bfloat16_rn(acc[e] * iv);
-                                else ws.o[((size_t)slot * 128 + rr) * D + d] = acc[e] * iv;
-                            }
+                        for (int e = 0; e < D / 32; ++e) {
+                            const int d = lane * (D / 32) + e;
+                            if (d < c0 || d >= c1) continue;
+                            if (whole) out_row(rr)[d] = __float2bfloat16_rn(acc[e] * iv);
+                            else ws.o[(size_t)(srow + rr) * D + d] = acc[e] * iv;
                         }
                     }
                 }
             }
             tc_fence_before();
-            named_bar_sync(kEpiBar, 256);  // both accumulators and (m, l) are read
-            n += cnt;
-            ++item;
-            if (!whole && it.j0 == 0) desc = make_int4(it.q0, it.nrows, it.kvh, walk.pieces(it));  // the share's last item
+            if (!pair) named_bar_sync(kEpiBar, 256);  // both accumulators and (m, l) are read
+            n += steps;
+            kt += it.j1 - it.j0;
+            qc += it.rt;
+            if (!whole && it.j0 == 0)  // (the share's last item)
+                desc = make_int4(it.q0, min(2 * C::QPOS, it.T - it.r0) * G, it.kvh, walk.pieces(it));
         }
         if (tid == 0) ws.desc[blockIdx.x] = desc;
     }
@@ -874,13 +1064,16 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a, const
     const int4 d = ws.desc[g];
     const int np = d.w;
     if (np < 1 || g + np > ctas) return;
+#pragma unroll 1
     for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < d.y; r += gridDim.y * 4) {
-        auto at = [&](int p) { return (size_t)(2 * (g + p) + (p == 0 ? 1 : 0)) * 128 + r; };
+        auto at = [&](int p) { return (size_t)(2 * (g + p) + (p == 0 ? 1 : 0)) * 256 + r; };
         float m = -INFINITY, l = 0.f;
+#pragma unroll 1
         for (int p = lane; p < np; p += 32) m = fmaxf(m, __ldcg(ws.lse + at(p)));
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
         const float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
         for (int p = lane; p < np; p += 32) l += ex2(__ldcg(ws.lse + at(p)) - mb);
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
@@ -922,18 +1115,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// A tensor of `rank` dims (innermost first, `elem` bytes an element), boxes
-// of `box`.
-bool tiled_map(CUtensorMap *map, CUtensorMapDataType type, int elem, int rank, const void *base, const cuuint64_t *dims,
-               const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
+// A tensor of `rank` dims (innermost first) with byte strides for all but the
+// first, copied in boxes of `box`.
+bool tiled_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
+               const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
     auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t strides[2] = {};
-    cuuint64_t s = elem;
-    for (int i = 0; i + 1 < rank; ++i) strides[i] = s *= dims[i];
-    const cuuint32_t ones[3] = {1, 1, 1};
-    return fn(map, type, rank, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return fn && fn(map, type, rank, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class C>
@@ -953,26 +1142,36 @@ cudaError_t run_tree(const TreeArgs &a, const TreeWs &ws, cudaStream_t st) {
         }
     }
     CUtensorMap tk, tv, tq = {};
-    const cuuint64_t cdims[2] = {(cuuint64_t)C::D, (cuuint64_t)a.num_blocks * a.Hkv * 16};
-    const cuuint32_t cbox[2] = {C::FP8 ? (cuuint32_t)C::D : 64u, 16};
-    const auto type = C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const auto swz = C::FP8 && C::D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    if (!tiled_map(&tk, type, C::FP8 ? 1 : 2, 2, a.k_cache, cdims, cbox, swz) ||
-        !tiled_map(&tv, type, C::FP8 ? 1 : 2, 2, a.v_cache, cdims, cbox, swz))
-        return cudaErrorInvalidValue;
-    if (!C::FP8) {
+    const cuuint64_t rows = (cuuint64_t)a.num_blocks * a.Hkv * 16;
+    bool ok;
+    if (C::FP8) {  // rows of D codes; a box is a block of one kv head
+        const cuuint64_t dims[2] = {(cuuint64_t)C::D, rows}, strides[1] = {(cuuint64_t)C::D};
+        const cuuint32_t box[2] = {(cuuint32_t)C::D, 16};
+        const auto swz = C::D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+        ok = tiled_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.k_cache, dims, strides, box, swz) &&
+             tiled_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.v_cache, dims, strides, box, swz);
+    } else {
+        const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const auto swz = CU_TENSOR_MAP_SWIZZLE_128B;
+        // 64 columns, 8 rows, column atoms, 8-row groups
+        const cuuint64_t dims[4] = {64, 8, (cuuint64_t)C::NATOM, rows / 8};
+        const cuuint64_t strides[3] = {(cuuint64_t)C::D * 2, 128, (cuuint64_t)C::D * 16};
+        const cuuint32_t box[4] = {64, 8, (cuuint32_t)C::NATOM, 2};
         const cuuint64_t qdims[3] = {(cuuint64_t)C::D, (cuuint64_t)a.Hq, (cuuint64_t)a.total_q};
+        const cuuint64_t qstrides[2] = {(cuuint64_t)C::D * 2, (cuuint64_t)a.Hq * C::D * 2};
         const cuuint32_t qbox[3] = {64, (cuuint32_t)C::G, (cuuint32_t)C::QPOS};
-        if (!tiled_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 3, a.q, qdims, qbox, CU_TENSOR_MAP_SWIZZLE_128B))
-            return cudaErrorInvalidValue;
+        ok = tiled_map(&tk, bf16, 4, a.k_cache, dims, strides, box, swz) &&
+             tiled_map(&tv, bf16, 4, a.v_cache, dims, strides, box, swz) &&
+             tiled_map(&tq, bf16, 3, a.q, qdims, qstrides, qbox, swz);
     }
+    if (!ok) return cudaErrorInvalidValue;
     // a CTA per SM, fewer where the batch has fewer key tiles
-    const long long tiles = (long long)a.B * a.Hkv * ((a.max_q_len + C::QPOS - 1) / C::QPOS) *
-                            ((a.max_blocks + C::BPT - 1) / C::BPT + kSegCost);
+    const long long tiles = (long long)a.B * a.Hkv * ((a.max_q_len + 2 * C::QPOS - 1) / (2 * C::QPOS)) *
+                            ((a.max_blocks + C::BPT - 1) / C::BPT);
     const int ctas = (int)std::min<long long>({tiles, sm_count(), kMaxCtas});
     e = launch_pdl(tree_kernel<C>, dim3(ctas), dim3(C::NT), C::SMEM, st, a, ws, tk, tv, tq);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tree_merge_kernel<C::D, C::G>, dim3(ctas, 8), dim3(128), 0, st, a, ws, ctas);
+    return launch_pdl(tree_merge_kernel<C::D, C::G>, dim3(ctas, 32), dim3(128), 0, st, a, ws, ctas);
 }
 
 template <int D, bool FP8>
@@ -986,11 +1185,11 @@ cudaError_t tree_by_group(const TreeArgs &a, const TreeWs &ws, cudaStream_t st) 
     }
 }
 
-constexpr size_t kLseBytes = 2 * kMaxCtas * 128 * sizeof(float), kDescBytes = kMaxCtas * sizeof(int4);
+constexpr size_t kLseBytes = 2 * kMaxCtas * 256 * sizeof(float), kDescBytes = kMaxCtas * sizeof(int4);
 
 }  // namespace
 
-size_t tree_ws_bytes(int D) { return kLseBytes + kDescBytes + (size_t)2 * kMaxCtas * 128 * D * sizeof(float); }
+size_t tree_ws_bytes(int D) { return kLseBytes + kDescBytes + (size_t)2 * kMaxCtas * 256 * D * sizeof(float); }
 
 cudaError_t launch_tree(const TreeArgs &a, void *workspace, cudaStream_t st) {
     char *p = static_cast<char *>(workspace);

@@ -87,7 +87,7 @@ struct TCfg {
     static constexpr int OFF_BAD = OFF_QEXP + (FP8 ? 4 * 128 : 0);  // E4M3: query exponents of 4 query tiles, a byte a row
     static constexpr int NBAD = 16;                        // ring of the key tiles' bad-block masks
     static constexpr int OFF_BAR = OFF_BAD + NBAD * 4;
-    static constexpr int NBAR = 2 * NSK + 2 * NSV + 6 + 5 + 2 * NST;
+    static constexpr int NBAR = 2 * NSK + 2 * NSV + 10 + 5 + 2 * NST;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;    // TMEM address, share start
     static constexpr int USED = OFF_MISC + 64;
     static constexpr int SLACK = USED + 1024 <= 227 * 1024 ? 1024 : 0;  // else the base must be aligned (checked)
@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(C::NT, 1)
     volatile uint32_t *badmask = reinterpret_cast<uint32_t *>(smem + C::OFF_BAD);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *kfull = bars, *kempty = kfull + NSK, *vfull = kempty + NSK, *vempty = vfull + NSV;
-    uint64_t *sfull = vempty + NSV, *pfull = sfull + 2, *odone = pfull + 2;
+    // per stream: scores; P of keys 0-63 (+ 2: of 64-127); P.V of keys 0-63; P.V whole
+    uint64_t *sfull = vempty + NSV, *pfull = sfull + 2, *ohalf = pfull + 4, *odone = ohalf + 2;
     uint64_t *qfull = odone + 2, *qempty = qfull + 2, *mma_done = qempty + 2;
     uint64_t *cfull = mma_done + 1, *cempty = cfull + NST;  // E4M3: staging ring of codes
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
@@ -392,6 +393,8 @@ __global__ void __launch_bounds__(C::NT, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sfull[s], 1);
             mbar_init(&pfull[s], 128);
+            mbar_init(&pfull[2 + s], 128);
+            mbar_init(&ohalf[s], 1);
             mbar_init(&odone[s], 1);
             mbar_init(&qfull[s], C::Q_ARRIVALS);
             mbar_init(&qempty[s], 1);
@@ -559,29 +562,30 @@ __global__ void __launch_bounds__(C::NT, 1)
             __syncwarp();
         }
     } else if (w == C::W_MMA) {
-        constexpr uint32_t idS = idesc_f16kind_f32(128, KT, false, !C::FP8);
-        constexpr uint32_t idO = idesc_f16kind_f32(128, D, true, !C::FP8);
-        // counters instead of divisions by ring sizes: this warp's own
-        // instructions between two MMAs are time that the tensor pipe waits
-        struct Ring {
-            int slot;
-            uint32_t phase;
-            PA_DEVICE void next(int n) {
-                if (++slot == n) slot = 0, phase ^= 1;
-            }
-        };
-        // operand descriptors of the rings' first tiles; an address is 16 bytes a unit
-        const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024), dk = smem_desc_sw128(smem_addr(sK), 16, C::GROUP),
-                       dv = smem_desc_sw128(smem_addr(sV), 1024, C::GROUP);
-        int n = 0, kt = 0, qc = 0;   // steps, key tiles and query tiles before this one
-        Ring kr{0, 0}, vr{0, 0};     // this step's K tile; the V tile of the step whose P.V is still to issue:
-        int pn = -1, pbad = 0, pkv0 = 0, pL = 0;
-        bool pfirst = false, plast = false;  // the first of its accumulator; the last to read its V tile
-        auto scores = [&](int qslot, bool last_k, bool last_q) {  // S(n) = Q K^T
-            wait(&kfull[kr.slot], kr.phase);
-            if (n >= 2) wait(&odone[n & 1], ((n >> 1) - 1) & 1);  // P(n-2), in S(n)'s columns, has been used
-            if (!agree()) return;
-            if (elect_one()) {
+        // ---- one thread issues the MMAs (a whole warp in step, with a vote
+        // after its waits, spent 1,500 clocks a step on itself)
+        bool done = true;
+        if (elect_one()) {
+            constexpr uint32_t idS = idesc_f16kind_f32(128, KT, false, !C::FP8);
+            constexpr uint32_t idO = idesc_f16kind_f32(128, D, true, !C::FP8);
+            struct Ring {  // slots in turn, without divisions
+                int slot;
+                uint32_t phase;
+                PA_DEVICE void next(int n) {
+                    if (++slot == n) slot = 0, phase ^= 1;
+                }
+            };
+            // operand descriptors of the rings' first tiles; an address is 16 bytes a unit
+            const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024),
+                           dk = smem_desc_sw128(smem_addr(sK), 16, C::GROUP),
+                           dv = smem_desc_sw128(smem_addr(sV), 1024, C::GROUP);
+            int n = 0, qc = 0;                   // steps and query tiles before this one
+            Ring kr{0, 0}, vr{0, 0};             // this step's K tile; the V tile of step n - 1
+            bool pfirst = false, plast = false;  // step n - 1: the first of its accumulator; the last to read its V tile
+            auto scores = [&](int qslot, bool last_k, bool last_q) {  // S(n) = Q K^T
+                wait(&kfull[kr.slot], kr.phase);
+                // P(n-2), in S(n)'s columns, has been used
+                if (n >= 2 ? !wait(&odone[n & 1], ((n >> 1) - 1) & 1) : !ok) return;
                 tc_fence_after();
                 const uint64_t a0 = dq + qslot * (C::TILE / 16), b0 = dk + kr.slot * (C::TILE / 16);
 #pragma unroll
@@ -591,82 +595,55 @@ __global__ void __launch_bounds__(C::NT, 1)
                 tc_commit(&sfull[n & 1]);
                 if (last_k) tc_commit(&kempty[kr.slot]);
                 if (last_q) tc_commit(&qempty[qslot]);
-            }
-            __syncwarp();
-        };
-        auto pv = [&] {  // O += P(pn) V
-            wait(&vfull[vr.slot], vr.phase);
-            if constexpr (!C::FP8) {  // rows past the end or of bad blocks: zero them before they meet P
-                const uint32_t bad = badmask[pbad % C::NBAD];
-                if (pkv0 + KT > pL || bad) {
-                    if (!agree()) return;
-                    uint8_t *vt = sV + vr.slot * C::TILE;
-#pragma unroll 1
-                    for (int r = lane; r < KT; r += 32)
-                        if (pkv0 + r >= pL || ((bad >> (r >> 4)) & 1))
-#pragma unroll
-                            for (int c = 0; c < C::NATOM * 8; ++c)
-                                *reinterpret_cast<uint4 *>(vt + (r >> 3) * C::GROUP + (r & 7) * 128 + (c / 8) * 1024 + (c % 8) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-            }
-            wait(&pfull[pn & 1], (pn >> 1) & 1);
-            if (!agree()) return;
-            if (elect_one()) {
-                tc_fence_after();
+            };
+            auto pv = [&] {  // O += P(n-1) V
+                wait(&vfull[vr.slot], vr.phase);
+                const int p = n - 1;
                 const uint64_t b0 = dv + vr.slot * (C::TILE / 16);
-                const uint32_t o0 = tmem + C::COL_O + (pn & 1) * D, p0 = tmem + (pn & 1) * KT;
+                const uint32_t o0 = tmem + C::COL_O + (p & 1) * D, p0 = tmem + (p & 1) * KT;
 #pragma unroll
-                for (int kk = 0; kk < KT / 16; ++kk)
-                    tc_mma_bf16_tmem_a(o0, p0 + kk * 8, b0 + kk * 2 * C::GROUP / 16, idO, !pfirst || kk > 0);
-                tc_commit(&odone[pn & 1]);
-                if (plast) tc_commit(&vempty[vr.slot]);
-            }
-            __syncwarp();
-            if (plast) vr.next(NSV);
-        };
-        bool more = walk.next(a, it), was_pair = false;
-#pragma unroll 1
-        while (more && ok) {
-            const int steps = it.steps(), pair = it.rt - 1;
-#pragma unroll 1
-            for (int k = 0; k < steps && ok; ++k, ++n) {
-                const int qt = pair ? k & 1 : 0, qslot = (qc + qt) & 1;
-                // the scores first, so that the tensor pipe has them while
-                // P(n-1) is computed; but where a new query tile takes the
-                // place of one that the last scores read, P.V first
-                const bool pv_first = k == 0 && (pair || was_pair);
-#pragma unroll 1
-                for (int u = 0; u < 2 && ok; ++u) {
-                    if ((u == 0) == pv_first) {
-                        if (pn >= 0) pv();
-                    } else {
-                        if (k <= pair) wait(&qfull[qslot], ((qc + qt) >> 1) & 1);
-                        scores(qslot, !pair || (k & 1), k >= steps - 1 - pair);
+                for (int kk = 0; kk < KT / 16; ++kk) {
+                    if (kk % (KT / 32) == 0) {  // each half as its P arrives
+                        if (kk > 0) tc_commit(&ohalf[p & 1]);
+                        if (!wait(&pfull[(kk > 0 ? 2 : 0) + (p & 1)], (p >> 1) & 1)) return;
+                        tc_fence_after();
                     }
+                    tc_mma_bf16_tmem_a(o0, p0 + kk * 8, b0 + kk * 2 * C::GROUP / 16, idO, !pfirst || kk > 0);
                 }
-                pn = n;
-                pkv0 = (it.j0 + (pair ? k >> 1 : k)) * KT;
-                pL = it.L;
-                pfirst = k < 2;
-                pbad = kt;
-                plast = !pair || (k & 1);
+                tc_commit(&odone[p & 1]);
                 if (plast) {
-                    kr.next(NSK);
-                    ++kt;
+                    tc_commit(&vempty[vr.slot]);
+                    vr.next(NSV);
                 }
+            };
+            bool more = walk.next(a, it), was_pair = false;
+#pragma unroll 1
+            while (more && ok) {
+                const int steps = it.steps(), pair = it.rt - 1;
+#pragma unroll 1
+                for (int k = 0; k < steps && ok; ++k, ++n) {
+                    const int qt = pair & k, qslot = (qc + qt) & 1;
+                    // the scores first, so that the tensor pipe has them while
+                    // P(n-1) is computed; but where a new query tile takes the
+                    // place of one that the last scores read, P.V first
+                    const bool pv_first = k == 0 && (pair || was_pair);
+                    if (pv_first && n > 0) pv();
+                    if (k <= pair) wait(&qfull[qslot], ((qc + qt) >> 1) & 1);
+                    scores(qslot, !pair || qt, k >= steps - 1 - pair);
+                    if (!pv_first && n > 0) pv();
+                    pfirst = k < 2;
+                    plast = !pair || qt;
+                    if (plast) kr.next(NSK);
+                }
+                qc += it.rt;
+                was_pair = pair;
+                more = ok && walk.next(a, it);
             }
-            qc += it.rt;
-            was_pair = pair;
-            more = ok && walk.next(a, it);
+            if (ok && n > 0) pv();
+            // every MMA of this CTA has completed before TMEM is released
+            tc_commit(mma_done);
+            done = mbar_wait(mma_done, 0, ok ? deadline : drain_deadline());
         }
-        if (ok && pn >= 0) pv();
-        // every MMA of this CTA has completed before TMEM is released
-        if (elect_one()) tc_commit(mma_done);
-        __syncwarp();
-        const bool done = mbar_wait(mma_done, 0, ok ? deadline : drain_deadline());
         ok = __all_sync(kFull, ok && done);
     } else if (w >= C::W_QUERY && w < C::W_WIDEN) {
         // ---- query tiles, two slots in turn.  bf16: warp 10, one 3-D box per
@@ -815,10 +792,23 @@ __global__ void __launch_bounds__(C::NT, 1)
         const uint32_t scol = lane_base + g * KT, ocol = lane_base + C::COL_O + g * D;
         int n = 0, kt = 0, qc = 0;
         int4 desc = make_int4(0, 0, 0, 0);
+        auto make_desc = [&](const Item &i) {  // (of the share's last item)
+            return make_int4(i.q0, min(2 * C::QPOS, i.T - i.r0) * G, i.kvh, walk.pieces(i));
+        };
 #pragma unroll 1
         while (walk.next(a, it)) {
             const int steps = it.steps(), pair = it.rt - 1;
             const int k0 = (n ^ g) & 1, qt = pair & k0;       // first step of this warpgroup, its row tile
+            // one stream alone holds a row's result: each row tile of two, or
+            // a single step (the other warpgroup goes on to the next item)
+            const bool solo = pair || steps == 1;
+            if (k0 >= steps) {
+                n += steps;
+                kt += it.j1 - it.j0;
+                qc += it.rt;
+                if (!it.whole() && it.j0 == 0) desc = make_desc(it);
+                continue;
+            }
             const int nrows = min(C::QPOS, it.T - it.r0 - qt * C::QPOS) * G;
             const bool warp_live = (w & 3) * 32 < nrows, row_live = r < nrows;
             const int64_t qrow = it.q0 + qt * C::QPOS + r / G;
@@ -830,124 +820,112 @@ __global__ void __launch_bounds__(C::NT, 1)
             for (int k = k0; k < steps; k += 2) {
                 const int nn = n + k, kv0 = (it.j0 + (pair ? k >> 1 : k)) * KT;
                 const bool landed = wait_all(&sfull[g], (nn >> 1) & 1);
-                if (landed && warp_live) {
-                    tc_fence_after();
-                    if (C::FP8 && k == k0)
-                        sl2 *= __uint_as_float((uint32_t)(127 - qexp[((qc + qt) & 3) * 128 + r]) << 23);
-                    // the keys this row may see, where the tile is not all prefix
-                    const uint32_t bad = badmask[(kt + (pair ? k >> 1 : k)) % C::NBAD];
-                    const bool masked = kv0 + KT > it.P || bad;
-                    // scores of keys kv0 + CW h + [0, CW), requested, and masked once they are there
-                    constexpr int CW = C::FP8 ? 16 : 32;  // (an E4M3 CTA's threads have fewer registers)
-                    auto request = [&](int h, float (&sv)[CW]) {
-                        if constexpr (CW == 32) tmem_ld32(scol + CW * h, sv);
-                        else tmem_ld16(scol + CW * h, sv);
-                    };
-                    auto mask = [&](int h, float (&sv)[CW]) {
-                        const int rel = kv0 + CW * h - it.P;  // draft of the first key
-                        const uint64_t seen = it.T < 64 ? bits & ((1ull << it.T) - 1) : bits;
-                        uint32_t v = rel <= -CW  ? kFull
-                                     : rel >= 64 ? 0u
-                                     : rel < 0   ? (uint32_t)((seen << -rel) | ((1ull << -rel) - 1))
-                                                 : (uint32_t)(seen >> rel);
-                        if ((bad >> (CW / 16 * h)) & 1) v &= 0xffff0000u;
-                        if (CW == 32 && ((bad >> (2 * h + 1)) & 1)) v &= 0x0000ffffu;
+                if (C::FP8 && landed && k == k0)
+                    sl2 *= __uint_as_float((uint32_t)(127 - qexp[((qc + qt) & 3) * 128 + r]) << 23);
+                const int t = kt + (pair ? k >> 1 : k);
+                const uint32_t bad = badmask[t % C::NBAD];
+                if constexpr (!C::FP8) {  // V rows past the end or of bad blocks: zero them before they meet P
+                    if (kv0 + KT > it.L || bad) {
+                        const bool there = wait_all(&vfull[t % NSV], (t / NSV) & 1);
+                        if (there && (kv0 + r >= it.L || ((bad >> (r >> 4)) & 1))) {
+                            uint8_t *vrow = sV + t % NSV * C::TILE + (r >> 3) * C::GROUP + (r & 7) * 128;
 #pragma unroll
-                        for (int e = 0; e < CW; ++e) sv[e] = v & (1u << e) ? sv[e] : -INFINITY;
-                    };
-                    auto largest = [&](const float (&sv)[CW], float mx) {
-#pragma unroll
-                        for (int e = 0; e < CW; e += 2) mx = fmax3(mx, sv[e], sv[e + 1]);
-                        return mx;
-                    };
-                    // the segment's first step takes its maximum beforehand;
-                    // later ones exponentiate against the maximum so far and
-                    // do it again in the rare case that a score exceeds it by
-                    // more than the threshold (P is held in registers, the
-                    // scores stay, until then)
-                    if (k == k0) {
-                        float mx = -INFINITY;
-#pragma unroll 1
-                        for (int h = 0; h < KT / CW; ++h) {
-                            float sv[CW];
-                            request(h, sv);
-                            tmem_wait_ld();
-                            if (masked) mask(h, sv);
-                            mx = largest(sv, mx);
+                            for (int c = 0; c < C::NATOM * 8; ++c)
+                                *reinterpret_cast<uint4 *>(vrow + (c / 8) * 1024 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
                         }
-                        m = mx * sl2;  // (the scale is positive)
+                        fence_proxy_async_smem();
                     }
-                    uint32_t pk[KT / 2];
-                    float2 sum;
+                }
+                // the keys this row may see, where the tile is not all prefix
+                const bool masked = kv0 + KT > it.P || bad;
+                // half a tile at a time: P.V of the first 64 keys runs while
+                // the second 64 are exponentiated
 #pragma unroll 1
-                    for (;;) {
-                        const float nb = (m == -INFINITY ? 0.f : -m) + C::PBIAS;
-                        const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(nb, nb);
-                        float mx = -INFINITY;
-                        sum = make_float2(0.f, 0.f);
-                        float sv[2][CW];  // two buffers: the next load is in flight during the arithmetic
-                        request(0, sv[0]);
+                for (int h = 0; h < 2; ++h) {
+                    if (ok && warp_live) {
+                        tc_fence_after();
+                        float sv[64];
 #pragma unroll
-                        for (int h = 0; h < KT / CW; ++h) {
-                            tmem_wait_ld();
-                            if (h + 1 < KT / CW) request(h + 1, sv[(h + 1) & 1]);
-                            float(&x)[CW] = sv[h & 1];
-                            if (masked) mask(h, x);
-                            mx = largest(x, mx);
+                        for (int q = 0; q < 2; ++q) {
+                            float x[32];
+                            tmem_ld32(scol + 64 * h + 32 * q, x);
 #pragma unroll
-                            for (int e = 0; e < CW; e += 2) {
-                                const float2 y = ffma2(make_float2(x[e], x[e + 1]), sc2, nb2);
-                                const float2 p = make_float2(ex2(y.x), ex2(y.y));
-                                sum = fadd2(sum, p);
-                                if constexpr (C::FP8) {
-                                    const __half2 hh = __floats2half2_rn(p.x, p.y);
-                                    pk[CW / 2 * h + e / 2] = *reinterpret_cast<const uint32_t *>(&hh);
-                                } else {
-                                    const __nv_bfloat162 bb = __floats2bfloat162_rn(p.x, p.y);
-                                    pk[CW / 2 * h + e / 2] = *reinterpret_cast<const uint32_t *>(&bb);
+                            for (int e = 0; e < 32; ++e) sv[32 * q + e] = x[e];
+                        }
+                        tmem_wait_ld();
+                        if (masked) {
+                            const uint64_t seen = it.T < 64 ? bits & ((1ull << it.T) - 1) : bits;
+                            const int rel = kv0 + 64 * h - it.P;  // draft of the first key
+                            uint64_t v = rel <= -64  ? ~0ull
+                                         : rel >= 64 ? 0ull
+                                         : rel < 0   ? (seen << -rel) | ((1ull << -rel) - 1)
+                                                     : seen >> rel;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if ((bad >> (4 * h + i)) & 1) v &= ~(0xffffull << (16 * i));
+                            const uint32_t vl = (uint32_t)v, vh = (uint32_t)(v >> 32);
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                sv[e] = (e < 32 ? vl : vh) & (1u << (e & 31)) ? sv[e] : -INFINITY;
+                        }
+                        float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            mx = fmax3(mx, sv[e], sv[e + 1]);
+                            my = fmax3(my, sv[32 + e], sv[33 + e]);
+                        }
+                        const float mt = fmaxf(mx, my) * sl2;  // (the scale is positive)
+                        const bool rescale = mt > m + kRescaleThreshold;
+                        if (__any_sync(kFull, rescale)) {
+                            const float alpha = rescale ? ex2(m - mt) : 1.f;  // m = -inf: 0
+                            if (rescale) m = mt;
+                            l2 = make_float2(l2.x * alpha, l2.y * alpha);
+                            // O holds P.V up to the half tile before: complete
+                            // for the first half (these scores were issued after it)
+                            if (h > 0) wait_all(&ohalf[g], (nn >> 1) & 1);
+                            if (ok && (h > 0 || k > k0)) {
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int q = 0; q < D / 16; ++q) {
+                                    float o[16];
+                                    tmem_ld16(ocol + 16 * q, o);
+                                    tmem_wait_ld();
+                                    uint32_t ou[16];
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * alpha);
+                                    tmem_st16_u(ocol + 16 * q, ou);
                                 }
                             }
                         }
-                        const float mt = mx * sl2;
-                        const bool rescale = mt > m + kRescaleThreshold;
-                        if (!__any_sync(kFull, rescale)) break;
-                        // O holds P.V up to this stream's previous step, complete
-                        // (this step's scores were issued after it)
-                        const float alpha = rescale ? ex2(m - mt) : 1.f;  // m = -inf: 0
-                        if (rescale) m = mt;
-                        l2 = make_float2(l2.x * alpha, l2.y * alpha);
-                        if (k > k0) {
-#pragma unroll 1
-                            for (int q = 0; q < D / 16; ++q) {
-                                float o[16];
-                                tmem_ld16(ocol + 16 * q, o);
-                                tmem_wait_ld();
-                                uint32_t ou[16];
+                        const float nb = (m == -INFINITY ? 0.f : -m) + C::PBIAS;
+                        const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(nb, nb);
+                        uint32_t pk[32];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * alpha);
-                                tmem_st16_u(ocol + 16 * q, ou);
+                        for (int e = 0; e < 64; e += 2) {
+                            const float2 y = ffma2(make_float2(sv[e], sv[e + 1]), sc2, nb2);
+                            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                            l2 = fadd2(l2, p);
+                            if constexpr (C::FP8) {
+                                const __half2 hh = __floats2half2_rn(p.x, p.y);
+                                pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hh);
+                            } else {
+                                const __nv_bfloat162 bb = __floats2bfloat162_rn(p.x, p.y);
+                                pk[e / 2] = *reinterpret_cast<const uint32_t *>(&bb);
                             }
                         }
+                        tmem_st32_u(scol + 32 * h, pk);  // over scores that this thread has read
+                        tmem_wait_st();
+                        tc_fence_before();
                     }
-                    l2 = fadd2(l2, sum);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // P over the scores, all of which this thread has read
-                        uint32_t half[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) half[e] = pk[32 * h + e];
-                        tmem_st32_u(scol + 32 * h, half);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
+                    mbar_arrive(&pfull[2 * h + g]);
                 }
-                mbar_arrive(&pfull[g]);
             }
-            // ---- epilogue: two row tiles: this warpgroup's rows, all columns;
-            // one: the accumulators joined, columns [g D/2, (g+1) D/2)
+            // ---- epilogue: all columns of a stream alone, or the two
+            // accumulators joined, columns [g D/2, (g+1) D/2)
             const int last = n + steps - 1;  // the last step; the other stream's is last - 1
             float M = m, l = l2.x + l2.y, f0 = 1.f, f1 = 0.f;
             bool landed = true;
-            if (!pair) {
+            if (!solo) {
                 ml[g * 128 + r] = make_float2(m, l);
                 named_bar_sync(kEpiBar, 256);
                 const float2 ml0 = ml[r], ml1 = ml[128 + r];
@@ -959,17 +937,14 @@ __global__ void __launch_bounds__(C::NT, 1)
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
                 const int nn = last - u;
-                if ((pair && (nn & 1) != g) || (u == 1 && steps == 1)) continue;
+                if (solo && (nn & 1) != g) continue;
                 landed = wait_all(&odone[nn & 1], (nn >> 1) & 1);
             }
             const float inv = (l > 0.f ? 1.f / l : l == l ? 0.f : l) * C::OPMUL * (C::FP8 ? a.v_scale[it.kvh] : 1.f);
-            // accumulator A (first, in a pair this stream's), and B where both streams ran
-            const bool both = !pair && steps > 1;
-            const uint32_t colA = lane_base + C::COL_O + (pair ? g * D : both ? 0 : (last & 1) * D);
-            const uint32_t colB = both ? colA + D : colA;
+            const uint32_t colA = lane_base + C::COL_O + (solo ? g * D : 0), colB = solo ? colA : colA + D;
             const bool dead = l == 0.f;  // sees nothing: zeros
-            const float wA = (pair ? 1.f : both || !(last & 1) ? f0 : f1) * inv, wB = both ? f1 * inv : 0.f;
-            const int c0 = pair ? 0 : g * (D / 2), c1 = pair ? D : c0 + D / 2;
+            const float wA = f0 * inv, wB = f1 * inv;  // (alone: f0 = 1, f1 = 0)
+            const int c0 = solo ? 0 : g * (D / 2), c1 = solo ? D : c0 + D / 2;
             const bool whole = it.whole();
             const int slot = blockIdx.x * 2 + (it.j0 == 0 ? 1 : 0), srow = slot * 256 + qt * 128;
             auto out_row = [&](int rr) {
@@ -1009,7 +984,7 @@ __global__ void __launch_bounds__(C::NT, 1)
                             *reinterpret_cast<float4 *>(wo + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
-                if (!whole && row_live && (pair || g == 0))
+                if (!whole && row_live && (solo || g == 0))
                     ws.lse[srow + r] = l > 0.f ? M + lg2(l) - C::PBIAS : l == l ? -INFINITY : l;
                 // rows that an unseen draft's V spoilt
                 uint32_t todo = __ballot_sync(kFull, zero != 0.f && row_live && l > 0.f && l <= 3.4028235e38f);
@@ -1034,12 +1009,11 @@ __global__ void __launch_bounds__(C::NT, 1)
                 }
             }
             tc_fence_before();
-            if (!pair) named_bar_sync(kEpiBar, 256);  // both accumulators and (m, l) are read
+            if (!solo) named_bar_sync(kEpiBar, 256);  // both accumulators and (m, l) are read
             n += steps;
             kt += it.j1 - it.j0;
             qc += it.rt;
-            if (!whole && it.j0 == 0)  // (the share's last item)
-                desc = make_int4(it.q0, min(2 * C::QPOS, it.T - it.r0) * G, it.kvh, walk.pieces(it));
+            if (!whole && it.j0 == 0) desc = make_desc(it);
         }
         if (tid == 0) ws.desc[blockIdx.x] = desc;
     }

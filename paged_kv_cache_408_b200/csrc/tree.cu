@@ -150,7 +150,7 @@ struct Item {
     int b, kvh, q0, T, P, L;   // q0: first row of the segment; T: drafts of the sequence
     int r0, rt;                // first draft of the segment; its row tiles, 1 or 2
     int j0, j1, nt;            // nt: key tiles of the segment
-    int64_t tile0;             // line position of its first tile
+    int tile0;                 // line position of its first tile
     PA_DEVICE int steps() const { return (j1 - j0) * rt; }
     PA_DEVICE bool whole() const { return j0 == 0 && j1 == nt; }
 };
@@ -158,13 +158,12 @@ struct Item {
 // Walks a CTA's share of the line.
 template <class C>
 struct Walk {
-    int64_t pos, end, base;  // base: line position of sequence b
-    int64_t S;
-    int b;
+    int pos, end, base;  // base: line position of sequence b
+    int S, b;
     Seq s;
     Raw nxt;                 // sequence b + 1, loaded ahead
 
-    PA_DEVICE void start(const TreeArgs &a, int64_t pos_, int64_t end_, int64_t S_, int b0, int64_t base0) {
+    PA_DEVICE void start(const TreeArgs &a, int pos_, int end_, int S_, int b0, int base0) {
         pos = pos_, end = end_, S = S_, b = b0, base = base0;
         if (pos < end) {
             s = make_seq<C>(a, load_raw(a, b), false);
@@ -174,16 +173,14 @@ struct Walk {
     PA_DEVICE bool next(const TreeArgs &a, Item &it) {
 #pragma unroll 1
         while (pos < end) {
-            const int head = s.units_head();
-            const int64_t off64 = pos - base;
-            if (off64 >= (int64_t)head * a.Hkv) {
-                base += (int64_t)head * a.Hkv;
+            const int head = s.units_head(), off = pos - base;
+            if (off >= head * a.Hkv) {
+                base += head * a.Hkv;
                 s = make_seq<C>(a, nxt, false);
                 nxt = load_raw(a, ++b + 1);
                 continue;
             }
-            const unsigned off = (unsigned)off64;  // below 2^31: at most 128 kv heads x 3 segments x 2^24 units
-            it.kvh = off / (unsigned)head;
+            it.kvh = off / head;
             int r = off - it.kvh * head;           // unit within the kv head's segments, then within the segment
             const int Up = kSegCost + s.nt * kPair;
             int seg = r / Up;
@@ -191,11 +188,11 @@ struct Walk {
             seg = min(seg, s.npair);
             r -= seg * Up;
             const int wt = it.rt == 2 ? kPair : kOne, U = kSegCost + s.nt * wt;
-            const int stop = (int)min((int64_t)U, end - pos + r);
+            const int stop = min(U, end - pos + r);
             // the tiles whose first unit lies in the share
             it.j0 = max(0, r - kSegCost + wt - 1) / wt;
             it.j1 = max(0, stop - kSegCost + wt - 1) / wt;
-            const int64_t seg0 = pos - r;
+            const int seg0 = pos - r;
             pos = seg0 + stop;
             if (it.j1 <= it.j0) continue;
             it.b = b;
@@ -213,8 +210,8 @@ struct Walk {
     // pieces of a segment: one for every share from the one that holds its
     // first tile's first unit to the one that holds its last tile's
     PA_DEVICE int pieces(const Item &it) const {
-        const int64_t last = it.tile0 + (int64_t)(it.nt - 1) * (it.rt == 2 ? kPair : kOne);
-        return (int)(last / S - it.tile0 / S) + 1;
+        const int last = it.tile0 + (it.nt - 1) * (it.rt == 2 ? kPair : kOne);
+        return last / S - it.tile0 / S + 1;
     }
 };
 
@@ -285,6 +282,16 @@ PA_DEVICE void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
     asm("mad.lo.u32 %0, %1, 128, %0;" : "+r"(lo) : "r"(a & 0x00800080u));
     asm("mul.lo.u32 %0, %1, 128;" : "=r"(hi) : "r"(b));
     asm("mad.lo.u32 %0, %1, 128, %0;" : "+r"(hi) : "r"(b & 0x00800080u));
+}
+
+// The same by the conversion instruction, for half of the words: that runs on
+// the exponentials' pipe, which the integer forms leave idle.
+PA_DEVICE void widen4_cvt(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const __half2 s = __floats2half2_rn(0x1p-8f, 0x1p-8f);  // (exact: the smallest code is 2^-9)
+    const uint32_t l = e4m3x2_to_h2(w), h = e4m3x2_to_h2(w >> 16);
+    const __half2 a = __hmul2(*reinterpret_cast<const __half2 *>(&l), s), b = __hmul2(*reinterpret_cast<const __half2 *>(&h), s);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
 }
 
 // Chunks 2u and 2u + 1 (8 f16 each) of a swizzled operand row.
@@ -368,9 +375,9 @@ __global__ void __launch_bounds__(C::NT, 1)
     uint64_t *cfull = mma_done + 1, *cempty = cfull + NST;  // E4M3: staging ring of codes
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     int *s_b0 = reinterpret_cast<int *>(smem + C::OFF_MISC + 4);
-    int64_t *s_base = reinterpret_cast<int64_t *>(smem + C::OFF_MISC + 8);  // base of b0; share size; total
+    int *s_base = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);  // base of b0; share size; total
     // scan scratch: in the (m, l) area, which is not in use yet
-    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::OFF_ML);
+    int *scan = reinterpret_cast<int *>(smem + C::OFF_ML);
 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     pdl_trigger();
@@ -412,31 +419,31 @@ __global__ void __launch_bounds__(C::NT, 1)
     // ---- the share of this CTA: a scan over the sequences' line units
     {
         const int per = (a.B + C::NT - 1) / C::NT, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-        int64_t mine = 0;
+        int mine = 0;  // (the whole line has less than 2^31 units: checked on the host)
 #pragma unroll 1
         for (int b = b0; b < b1; ++b)
-            mine += (int64_t)make_seq<C>(a, load_raw(a, b), blockIdx.x == 0).units_head() * a.Hkv;
-        int64_t x = mine;
+            mine += make_seq<C>(a, load_raw(a, b), blockIdx.x == 0).units_head() * a.Hkv;
+        int x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(kFull, x, o);
+            const int y = __shfl_up_sync(kFull, x, o);
             if (lane >= o) x += y;
         }
         if (lane == 31) scan[w] = x;
         __syncthreads();
-        int64_t before = x - mine, total = 0;
+        int before = x - mine, total = 0;
 #pragma unroll
         for (int i = 0; i < C::NT / 32; ++i) {
             if (i < w) before += scan[i];
             total += scan[i];
         }
-        const int64_t S = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kPair);  // at least a tile's units
-        const int64_t pos = (int64_t)blockIdx.x * S;
+        const int S = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kPair);  // at least a tile's units
+        const int64_t pos = (int64_t)blockIdx.x * S;  // (may lie past the line)
         if (pos >= before && pos < before + mine) {  // one thread at most
-            int64_t at = before;
+            int at = before;
             int b = b0;
             for (;; ++b) {
-                const int64_t u = (int64_t)make_seq<C>(a, load_raw(a, b), false).units_head() * a.Hkv;
+                const int u = make_seq<C>(a, load_raw(a, b), false).units_head() * a.Hkv;
                 if (pos < at + u) break;
                 at += u;
             }
@@ -455,8 +462,8 @@ __global__ void __launch_bounds__(C::NT, 1)
     const uint32_t tmem = *tmem_slot;
     Walk<C> walk;
     {
-        const int64_t S = s_base[1], total = s_base[2], pos = min((int64_t)blockIdx.x * S, total);
-        walk.start(a, pos, min(pos + S, total), S, *s_b0, s_base[0]);
+        const int S = s_base[1], total = s_base[2], pos = (int)min((int64_t)blockIdx.x * S, (int64_t)total);
+        walk.start(a, pos, min(total - pos, S) + pos, S, *s_b0, s_base[0]);
     }
     __syncthreads();  // the scan scratch is free
     // ok turns false at the first wait past the deadline; after that a role
@@ -750,6 +757,10 @@ __global__ void __launch_bounds__(C::NT, 1)
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
+                        if (e & 1) {
+                            widen4_cvt(wd[e], h[2 * e], h[2 * e + 1]);
+                            continue;
+                        }
                         widen4(wd[e], h[2 * e], h[2 * e + 1]);
                         nan |= (wd[e] & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a byte: its code is a NaN
                     }
@@ -899,21 +910,24 @@ __global__ void __launch_bounds__(C::NT, 1)
                         }
                         const float nb = (m == -INFINITY ? 0.f : -m) + C::PBIAS;
                         const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(nb, nb);
-                        uint32_t pk[32];
 #pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const float2 y = ffma2(make_float2(sv[e], sv[e + 1]), sc2, nb2);
-                            const float2 p = make_float2(ex2(y.x), ex2(y.y));
-                            l2 = fadd2(l2, p);
-                            if constexpr (C::FP8) {
-                                const __half2 hh = __floats2half2_rn(p.x, p.y);
-                                pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hh);
-                            } else {
-                                const __nv_bfloat162 bb = __floats2bfloat162_rn(p.x, p.y);
-                                pk[e / 2] = *reinterpret_cast<const uint32_t *>(&bb);
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 32 * q; e < 32 * q + 32; e += 2) {
+                                const float2 y = ffma2(make_float2(sv[e], sv[e + 1]), sc2, nb2);
+                                const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                                l2 = fadd2(l2, p);
+                                if constexpr (C::FP8) {
+                                    const __half2 hh = __floats2half2_rn(p.x, p.y);
+                                    pk[e / 2 - 16 * q] = *reinterpret_cast<const uint32_t *>(&hh);
+                                } else {
+                                    const __nv_bfloat162 bb = __floats2bfloat162_rn(p.x, p.y);
+                                    pk[e / 2 - 16 * q] = *reinterpret_cast<const uint32_t *>(&bb);
+                                }
                             }
+                            tmem_st16_u(scol + 32 * h + 16 * q, pk);  // over scores that this thread has read
                         }
-                        tmem_st32_u(scol + 32 * h, pk);  // over scores that this thread has read
                         tmem_wait_st();
                         tc_fence_before();
                     }
@@ -1139,10 +1153,11 @@ cudaError_t run_tree(const TreeArgs &a, const TreeWs &ws, cudaStream_t st) {
              tiled_map(&tq, bf16, 3, a.q, qdims, qstrides, qbox, swz);
     }
     if (!ok) return cudaErrorInvalidValue;
-    // a CTA per SM, fewer where the batch has fewer key tiles
-    const long long tiles = (long long)a.B * a.Hkv * ((a.max_q_len + 2 * C::QPOS - 1) / (2 * C::QPOS)) *
-                            ((a.max_blocks + C::BPT - 1) / C::BPT);
-    const int ctas = (int)std::min<long long>({tiles, sm_count(), kMaxCtas});
+    // a CTA per SM, fewer where the batch has fewer key tiles; the most line units the batch can have, with tables of this width
+    const long long groups = (a.max_q_len + 2 * C::QPOS - 1) / (2 * C::QPOS);
+    const long long tiles_wide = (a.max_blocks + C::BPT - 1) / C::BPT;
+    if ((long long)a.B * a.Hkv * groups * (kSegCost + kPair * tiles_wide) > INT32_MAX) return cudaErrorNotSupported;
+    const int ctas = (int)std::min<long long>({(long long)a.B * a.Hkv * groups * tiles_wide, sm_count(), kMaxCtas});
     e = launch_pdl(tree_kernel<C>, dim3(ctas), dim3(C::NT), C::SMEM, st, a, ws, tk, tv, tq);
     if (e != cudaSuccess) return e;
     return launch_pdl(tree_merge_kernel<C::D, C::G>, dim3(ctas, 32), dim3(128), 0, st, a, ws, ctas);

@@ -12,7 +12,7 @@
 // heads of a kv head; a segment is (sequence, kv head, one or two row tiles),
 // so K and V are read from HBM once per sequence (further segments, T G >
 // 256, find them in L2).  The segments' key tiles (128 keys, 8 blocks) form
-// one line of cost units (kSegCost at the head of a segment, kOne or kPair a
+// one line of cost units (SEG at the head of a segment, kOne or kPair a
 // tile), cut into equal contiguous shares, one per SM.  Of the segments a
 // CTA meets only its first can have begun before its share and only its last
 // can go on behind it, so two slots a CTA hold every partial result, whatever
@@ -50,9 +50,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the running maximum may lag behind
-// line units: per segment (epilogue, first tile), per key tile of a segment
-// of one and of two row tiles
-constexpr int kSegCost = 4, kOne = 2, kPair = 3;
+// line units of a key tile, in a segment of one and of two row tiles
+constexpr int kOne = 2, kPair = 3;
 constexpr int kMaxCtas = 160;              // partial-result slots: two a CTA
 constexpr int kEpiBar = 1;                 // named barrier of the softmax warps
 constexpr unsigned kFull = 0xffffffffu;
@@ -96,6 +95,10 @@ struct TCfg {
     // warps 0-7: softmax; 10 (E4M3: and 11): query tiles
     static constexpr int W_LOAD = 8, W_MMA = 9, W_QUERY = 10, W_WIDEN = 12;
     static constexpr int NT = (12 + NWIDEN) * 32;
+    // line units of a segment itself (its query tile, first tile and epilogue):
+    // 64 x 100 tokens take 3.0 us a segment of one tile against 1.45 us a tile
+    // (bf16), 8 against 2 us (E4M3)
+    static constexpr int SEG = FP8 ? 7 : 5;
     static constexpr uint32_t COL_O = 2 * KT;
     static constexpr uint32_t KV_ARRIVALS = FP8 ? NWIDEN * 32 : 1, Q_ARRIVALS = FP8 ? 64 : 1;  // that fill a tile
     static constexpr float OPMUL = FP8 ? 256.f : 1.f;  // E4M3: K and V operands are 2^-8 of their value (widen4)
@@ -120,7 +123,7 @@ struct Raw {
 struct Seq {
     int q0, T, P;          // first row, drafts (0 if its metadata is bad), prefix
     int nt, npair, none;   // key tiles; segments of two and of one row tile per kv head
-    PA_DEVICE int units_head() const { return npair * (kSegCost + nt * kPair) + none * (kSegCost + nt * kOne); }
+    PA_DEVICE int units_head(int seg) const { return npair * (seg + nt * kPair) + none * (seg + nt * kOne); }
 };
 
 PA_DEVICE Raw load_raw(const TreeArgs &a, int b) {
@@ -173,7 +176,7 @@ struct Walk {
     PA_DEVICE bool next(const TreeArgs &a, Item &it) {
 #pragma unroll 1
         while (pos < end) {
-            const int head = s.units_head(), off = pos - base;
+            const int head = s.units_head(C::SEG), off = pos - base;
             if (off >= head * a.Hkv) {
                 base += head * a.Hkv;
                 s = make_seq<C>(a, nxt, false);
@@ -182,16 +185,16 @@ struct Walk {
             }
             it.kvh = off / head;
             int r = off - it.kvh * head;           // unit within the kv head's segments, then within the segment
-            const int Up = kSegCost + s.nt * kPair;
+            const int Up = C::SEG + s.nt * kPair;
             int seg = r / Up;
             it.rt = seg < s.npair ? 2 : 1;
             seg = min(seg, s.npair);
             r -= seg * Up;
-            const int wt = it.rt == 2 ? kPair : kOne, U = kSegCost + s.nt * wt;
+            const int wt = it.rt == 2 ? kPair : kOne, U = C::SEG + s.nt * wt;
             const int stop = min(U, end - pos + r);
             // the tiles whose first unit lies in the share
-            it.j0 = max(0, r - kSegCost + wt - 1) / wt;
-            it.j1 = max(0, stop - kSegCost + wt - 1) / wt;
+            it.j0 = max(0, r - C::SEG + wt - 1) / wt;
+            it.j1 = max(0, stop - C::SEG + wt - 1) / wt;
             const int seg0 = pos - r;
             pos = seg0 + stop;
             if (it.j1 <= it.j0) continue;
@@ -202,7 +205,7 @@ struct Walk {
             it.P = s.P;
             it.L = s.P + s.T;
             it.nt = s.nt;
-            it.tile0 = seg0 + kSegCost;
+            it.tile0 = seg0 + C::SEG;
             return true;
         }
         return false;
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(C::NT, 1)
         int mine = 0;  // (the whole line has less than 2^31 units: checked on the host)
 #pragma unroll 1
         for (int b = b0; b < b1; ++b)
-            mine += make_seq<C>(a, load_raw(a, b), blockIdx.x == 0).units_head() * a.Hkv;
+            mine += make_seq<C>(a, load_raw(a, b), blockIdx.x == 0).units_head(C::SEG) * a.Hkv;
         int x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(C::NT, 1)
             int at = before;
             int b = b0;
             for (;; ++b) {
-                const int u = make_seq<C>(a, load_raw(a, b), false).units_head() * a.Hkv;
+                const int u = make_seq<C>(a, load_raw(a, b), false).units_head(C::SEG) * a.Hkv;
                 if (pos < at + u) break;
                 at += u;
             }
@@ -1156,7 +1159,7 @@ cudaError_t run_tree(const TreeArgs &a, const TreeWs &ws, cudaStream_t st) {
     // a CTA per SM, fewer where the batch has fewer key tiles; the most line units the batch can have, with tables of this width
     const long long groups = (a.max_q_len + 2 * C::QPOS - 1) / (2 * C::QPOS);
     const long long tiles_wide = (a.max_blocks + C::BPT - 1) / C::BPT;
-    if ((long long)a.B * a.Hkv * groups * (kSegCost + kPair * tiles_wide) > INT32_MAX) return cudaErrorNotSupported;
+    if ((long long)a.B * a.Hkv * groups * (C::SEG + kPair * tiles_wide) > INT32_MAX) return cudaErrorNotSupported;
     const int ctas = (int)std::min<long long>({(long long)a.B * a.Hkv * groups * tiles_wide, sm_count(), kMaxCtas});
     e = launch_pdl(tree_kernel<C>, dim3(ctas), dim3(C::NT), C::SMEM, st, a, ws, tk, tv, tq);
     if (e != cudaSuccess) return e;

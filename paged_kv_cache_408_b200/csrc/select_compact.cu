@@ -17,10 +17,12 @@
 //     one ordered count of both kinds gives every place, and the result does
 //     not depend on the order in which threads or atomics run.
 //   * The row is read from HBM once: its keys stay in shared memory for the
-//     later passes (what does not fit is read again through L2).  Long rows
-//     are spread over a thread-block cluster: each CTA keeps a contiguous
-//     part, the histograms and the counts are added over distributed shared
-//     memory.
+//     later passes (what does not fit is read again through L2).  Rows of
+//     more than 4096 tokens are spread over a thread-block cluster: each CTA
+//     keeps a contiguous part and adds its histogram to the first CTA's
+//     through distributed shared memory (one word a bin and CTA; every CTA
+//     reading every other's histogram was 32 remote loads a thread and pass,
+//     82 us for 4 x 65536 tokens against LARGE_US now).
 //   * Bound: the chain of passes (latency), not bytes: 4 B per token.
 //
 // Compact (pa_compact_kv): token keep[i] of a row moves to position
@@ -31,10 +33,12 @@
 // overwritten before it was read.
 //   * One cluster per (sequence, kv head); its CTAs read one group of
 //     consecutive entries together into registers, meet at the cluster
-//     barrier, and write.  The next group is read before the barrier: its
-//     sources lie above every destination of the current group.
-//   * 16-byte vectors; a thread moves the same vector of K and V, so the
-//     list and the block table are looked up once for both.
+//     barrier, and write.  The next group's sources lie above every
+//     destination of this one, so its reads need no second barrier.
+//   * The list and the block table are two dependent reads before any data
+//     can be: a CTA resolves 512 entries at a time into cache rows in shared
+//     memory, so that the groups' reads wait for nothing.
+//   * 16-byte vectors; a thread moves the same vector of K and V.
 //   * Entries that are in place already are skipped.
 //   * Bound: HBM, each moved row read and written once.
 #include <algorithm>
@@ -67,6 +71,22 @@ PA_DEVICE int dsmem_load(const int *p, uint32_t rank) {
     return v;
 }
 
+PA_DEVICE int4 dsmem_load4(const int *p, uint32_t rank) {
+    uint32_t a;
+    int4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+PA_DEVICE void dsmem_add(const int *p, uint32_t rank, int v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // Launch with a cluster of `c` CTAs along x, as a programmatic dependent.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int c, int threads, size_t smem, cudaStream_t st,
@@ -90,8 +110,6 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int c, int threa
 }
 
 // -------------------------------------------------------------------- select
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelCap = 16384;  // keys a CTA keeps in shared memory (64 KB)
 constexpr int kBins = 2048;     // 11-bit digits
 constexpr unsigned kFullMask = 0xffffffffu;
@@ -103,15 +121,18 @@ PA_DEVICE uint32_t order_key(float f) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+template <int THREADS>
 struct SelectSmem {
-    int hist[3][kBins];
-    int warp_a[kSelWarps], warp_b[kSelWarps];
+    alignas(16) int hist[3][kBins];
+    int warp_a[THREADS / 32], warp_b[THREADS / 32];
     int digit, above;      // digit of the k-th key in this pass; keys above it
     int cta_a, cta_b;      // this CTA's counts, read by the cluster
 };
 
-// Sum of `v` over the threads before this one (exclusive), and over all.
-PA_DEVICE int block_exclusive(int v, int *warp_sums, int tid, int *total) {
+// Sum of `v` over the threads before this one.  (The caller synchronises
+// before warp_sums is used again.)
+template <int THREADS>
+PA_DEVICE int block_exclusive(int v, int *warp_sums, int tid) {
     const int lane = tid & 31, w = tid >> 5;
     int x = v;
 #pragma unroll
@@ -121,21 +142,16 @@ PA_DEVICE int block_exclusive(int v, int *warp_sums, int tid, int *total) {
     }
     if (lane == 31) warp_sums[w] = x;
     __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
-        const int s = warp_sums[i];
-        before += i < w ? s : 0;
-        all += s;
-    }
-    __syncthreads();
-    *total = all;
-    return before + x - v;
+    // lane i sums warp i's total where warp i lies before this one
+    const int s = lane < w && lane < THREADS / 32 ? warp_sums[lane] : 0;
+    return __reduce_add_sync(kFullMask, s) + x - v;
 }
 
+template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
-    extern __shared__ uint32_t keys[];  // [kSelCap] keys of this CTA's part
-    __shared__ SelectSmem sm;
+    constexpr int kSelWarps = kSelThreads / 32, BPT = kBins / kSelThreads;  // BPT: bins a thread sums
+    extern __shared__ uint32_t keys[];  // keys of this CTA's part, up to kSelCap
+    __shared__ SelectSmem<kSelThreads> sm;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int C = gridDim.x, rank = C > 1 ? (int)cluster_rank() : 0;
     const int h = blockIdx.y, b = blockIdx.z;
@@ -206,27 +222,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
                         atomicAdd(&sm.hist[pass][(e[x] >> shift) & mask], 1);
             }
         }
-        if (C > 1) cluster_sync();
-        else __syncthreads();
-        // thread t sums the cluster's bins of 4 digits, highest digits first
-        int bin[4], sum = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int d = kBins - 1 - (4 * tid + x);
-            bin[x] = 0;
-            if (C > 1) {
-                for (int r = 0; r < C; ++r) bin[x] += dsmem_load(&sm.hist[pass][d], r);
-            } else {
-                bin[x] = sm.hist[pass][d];
-            }
-            sum += bin[x];
+        __syncthreads();
+        if (C > 1) {  // add this CTA's bins to the first CTA's
+            if (rank > 0)
+                for (int i = tid; i < kBins; i += kSelThreads)
+                    if (sm.hist[pass][i]) dsmem_add(&sm.hist[pass][i], 0, sm.hist[pass][i]);
+            cluster_sync();
         }
-        int total;
-        int above = block_exclusive(sum, sm.warp_a, tid, &total);  // keys with a higher digit
+        // thread t sums the bins of BPT digits, highest digits first
+        int bin[BPT], sum = 0;
+        const int d0 = kBins - BPT * (tid + 1);  // its lowest digit
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < BPT; x += 4) {
+            const int4 v = C > 1 ? dsmem_load4(&sm.hist[pass][d0 + x], 0) : *reinterpret_cast<const int4 *>(&sm.hist[pass][d0 + x]);
+            bin[x] = v.x, bin[x + 1] = v.y, bin[x + 2] = v.z, bin[x + 3] = v.w;
+            sum += v.x + v.y + v.z + v.w;
+        }
+        int above = block_exclusive<kSelThreads>(sum, sm.warp_a, tid);  // keys with a higher digit
+#pragma unroll
+        for (int x = BPT - 1; x >= 0; --x) {
             if (above < need && above + bin[x] >= need) {
-                sm.digit = kBins - 1 - (4 * tid + x);
+                sm.digit = d0 + x;
                 sm.above = above;
             }
             above += bin[x];
@@ -275,10 +291,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
             sm.cta_b = eall;
         }
         cluster_sync();
-        for (int r = 0; r < rank; ++r) {
-            gbefore += dsmem_load(&sm.cta_a, r);
-            ebefore += dsmem_load(&sm.cta_b, r);
-        }
+        const int ga = lane < rank ? dsmem_load(&sm.cta_a, lane) : 0, ea = lane < rank ? dsmem_load(&sm.cta_b, lane) : 0;
+        gbefore += __reduce_add_sync(kFullMask, ga);
+        ebefore += __reduce_add_sync(kFullMask, ea);
     }
     for (int qb = wq0; qb < wq1; qb += 32) {
         const int q = qb + lane;
@@ -321,18 +336,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
 
 // ------------------------------------------------------------------- compact
 constexpr int kCmpThreads = 256;
-constexpr int kCmpVec = 4;  // K (and V) vectors a thread moves per group
+constexpr int kCmpCtas = 4;     // CTAs an SM: one's reads run during another's barrier and writes
+constexpr int kCmpVec = 4;      // K (and V) vectors a thread moves per group
+constexpr int kCmpList = 512;   // entries a CTA resolves at a time
 
 template <int VPR>  // 16-byte vectors per token row
-__global__ void __launch_bounds__(kCmpThreads) compact_kernel(const CompactArgs a) {
-    constexpr int U = kCmpVec, TOK = kCmpThreads / VPR;  // tokens per vector index u
+__global__ void __launch_bounds__(kCmpThreads, kCmpCtas) compact_kernel(const CompactArgs a) {
+    // TOK: entries a vector index u covers; GRP: entries a CTA reads per group
+    constexpr int U = kCmpVec, TOK = kCmpThreads / VPR, GRP = U * TOK, NG = kCmpList / GRP;
+    __shared__ int64_t s_src[2][kCmpList], s_dst[2][kCmpList];  // cache rows; dst -1: nothing to move
     const int tid = threadIdx.x, vec = tid % VPR, tsub = tid / VPR;
     const int C = gridDim.x, rank = C > 1 ? (int)cluster_rank() : 0;
     const int h = blockIdx.y, b = blockIdx.z;
     pdl_trigger();
     pdl_wait();
     const int64_t cap = (int64_t)a.max_blocks * 16;
-    int n = a.keep_lens[b];
+    const int n = a.keep_lens[b];
     const int64_t start = a.start ? a.start[b] : 0;
     if (n < 0 || n > a.max_keep || start < 0 || start + n > cap) {  // uniform over the cluster
         if (tid == 0 && rank == 0) flag_error(a.err, PA_DEVERR_BAD_LEN);
@@ -342,80 +361,91 @@ __global__ void __launch_bounds__(kCmpThreads) compact_kernel(const CompactArgs 
     const int32_t *bt = a.block_tables + (size_t)b * a.max_blocks;
     uint4 *kc = static_cast<uint4 *>(a.k_cache), *vc = static_cast<uint4 *>(a.v_cache);
 
+    // this CTA's groups are g C + rank, GRP entries each; group g's rows in
+    // buffer (g / NG) % 2
+    auto resolve = [&](int g0) {  // groups g0 .. g0 + NG - 1
+#pragma unroll
+        for (int e = tid; e < kCmpList; e += kCmpThreads) {
+            const int64_t i = ((int64_t)(g0 + e / GRP) * C + rank) * GRP + e % GRP;
+            int64_t src = -1, dst = -1;
+            if (i < n) {
+                const int64_t p = keep[i], to = start + i, prev = i > 0 ? keep[i - 1] : -1;
+                if (p < to || p >= cap || prev >= p) {
+                    flag_error(a.err, PA_DEVERR_BAD_PAIR);
+                } else if (p != to) {
+                    const int64_t sb = bt[p >> 4], db = bt[to >> 4];
+                    if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
+                        flag_error(a.err, PA_DEVERR_BAD_BLOCK);
+                    } else {
+                        src = (sb * a.Hkv + h) * 16 + (p & 15);
+                        dst = (db * a.Hkv + h) * 16 + (to & 15);
+                    }
+                }
+            }
+            s_src[g0 / NG & 1][e] = src;
+            s_dst[g0 / NG & 1][e] = dst;
+        }
+        __syncthreads();
+    };
     struct Group {
         uint4 k[U], v[U];
         float wt[U];
-        int64_t dst[U];  // destination row, or -1: nothing to move
+        int64_t dst[U];
     };
-    auto row_of = [&](int64_t pos) -> int64_t {  // cache row of a position, or -1
-        const int64_t blk = bt[pos >> 4];
-        if (blk < 0 || blk >= a.num_blocks) {
-            flag_error(a.err, PA_DEVERR_BAD_BLOCK);
-            return -1;
-        }
-        return (blk * a.Hkv + h) * 16 + (pos & 15);
-    };
-    // entries [i0, i0 + U * TOK) of the list, read into registers
-    auto load = [&](int64_t i0, Group &g) {
-        int64_t src[U];
+    auto load = [&](int g, Group &x) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u * TOK + tsub;
-            src[u] = -1;
-            g.dst[u] = -1;
-            if (i < n) {
-                const int64_t p = keep[i], to = start + i;
-                if (p < to || p >= cap || (i > 0 && keep[i - 1] >= p)) {
-                    flag_error(a.err, PA_DEVERR_BAD_PAIR);
-                } else if (p != to) {
-                    src[u] = row_of(p);
-                    g.dst[u] = src[u] < 0 ? -1 : row_of(to);
-                }
+            const int e = g % NG * GRP + u * TOK + tsub;
+            const int64_t src = s_src[g / NG & 1][e];
+            x.dst[u] = s_dst[g / NG & 1][e];
+            if (x.dst[u] >= 0) {
+                x.k[u] = kc[src * VPR + vec];
+                x.v[u] = vc[src * VPR + vec];
+                if (a.weights && vec == 0) x.wt[u] = a.weights[src];
             }
         }
+    };
+    auto store = [&](const Group &x) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (g.dst[u] >= 0) {
-                g.k[u] = kc[src[u] * VPR + vec];
-                g.v[u] = vc[src[u] * VPR + vec];
-                if (a.weights && vec == 0) g.wt[u] = a.weights[src[u]];
+            if (x.dst[u] >= 0) {
+                kc[x.dst[u] * VPR + vec] = x.k[u];
+                vc[x.dst[u] * VPR + vec] = x.v[u];
+                if (a.weights && vec == 0) a.weights[x.dst[u]] = x.wt[u];
             }
     };
-    auto store = [&](const Group &g) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (g.dst[u] >= 0) {
-                kc[g.dst[u] * VPR + vec] = g.k[u];
-                vc[g.dst[u] * VPR + vec] = g.v[u];
-                if (a.weights && vec == 0) a.weights[g.dst[u]] = g.wt[u];
-            }
-    };
-    const int64_t step = (int64_t)C * U * TOK;
-    Group cur, nxt;
-    int64_t i0 = (int64_t)rank * U * TOK;
-    load(i0, cur);
-    for (int64_t base = 0; base < n; base += step) {  // the same trips in every CTA of the cluster
-        i0 += step;
-        load(i0, nxt);
+    const int groups = (int)(((int64_t)n + (int64_t)C * GRP - 1) / ((int64_t)C * GRP));  // the same in every CTA of the cluster
+    if (groups == 0) return;
+    for (int g = 0; g < groups; ++g) {
+        if (g % NG == 0) resolve(g);
+        Group x;
+        load(g, x);
         if (C > 1) cluster_sync();
         else __syncthreads();
-        store(cur);
-        cur = nxt;
+        store(x);
     }
 }
 
 template <int VPR>
 cudaError_t run_compact(const CompactArgs &a, cudaStream_t st) {
+    // CTAs a row: as many as its entries fill, while the grid stays within one
+    // wave
     const int group = kCmpVec * kCmpThreads / VPR;  // entries one CTA reads per group
     const long long rows = (long long)a.B * a.Hkv;
     int c = 1;
-    while (c < 8 && rows * c < 4LL * sm_count() && (long long)c * group < a.max_keep) c *= 2;
+    while (c < 8 && 2 * rows * c <= (long long)kCmpCtas * sm_count() && (long long)c * group < a.max_keep) c *= 2;
     return launch_cluster(compact_kernel<VPR>, dim3(c, a.Hkv, a.B), c, kCmpThreads, 0, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_select(const SelectArgs &a, cudaStream_t st) {
+    // rows of up to 4096 tokens: one CTA of 256 threads each (half the warps
+    // of 512, whose scans cost more than the tokens); longer ones: a cluster
+    // of CTAs of 512 threads, 4096 tokens each as far as 8 CTAs go
+    const int64_t cap = (int64_t)a.max_blocks * 16;
+    if (cap <= 4096)
+        return launch_cluster(select_kernel<256>, dim3(1, a.Hkv, a.B), 1, 256, (size_t)cap * 4, st, a);
     static std::mutex mu;
     static bool ready[64] = {};
     int dev = 0;
@@ -425,17 +455,15 @@ cudaError_t launch_select(const SelectArgs &a, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev]) {
-            e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
+            e = cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
             if (e != cudaSuccess) return e;
             ready[dev] = true;
         }
     }
-    // the longest row a CTA takes alone: 4096 tokens
-    const int64_t cap = (int64_t)a.max_blocks * 16;
-    int c = 1;
+    int c = 2;
     while (c < 8 && cap > (int64_t)c * 4096) c *= 2;
     const int64_t part = std::min<int64_t>(kSelCap, (cap + c - 1) / c + 4);
-    return launch_cluster(select_kernel, dim3(c, a.Hkv, a.B), c, kSelThreads, (size_t)((part + 3) / 4) * 16, st, a);
+    return launch_cluster(select_kernel<512>, dim3(c, a.Hkv, a.B), c, 512, (size_t)((part + 3) / 4) * 16, st, a);
 }
 
 cudaError_t launch_compact(const CompactArgs &a, cudaStream_t st) {

@@ -115,6 +115,22 @@ PA_DEVICE void bulk_g2s(void *dst_smem, const void *src_gmem, uint32_t bytes, ui
         : "memory");
 }
 
+// The same with an L2 eviction policy (l2_evict_first()).
+PA_DEVICE void bulk_g2s_hint(void *dst_smem, const void *src_gmem, uint32_t bytes, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_addr(dst_smem)),
+        "l"(src_gmem), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+// Policy of data that is read once: the first to leave L2.
+PA_DEVICE uint64_t l2_evict_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // Fetch the 128-byte line holding p into L2 (no register result, no wait).
 PA_DEVICE void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 

@@ -377,8 +377,14 @@ struct Producer {
             mbar_arrive_expect_tx(&bars[s], 2 * C::BLKB);
             const size_t src = ((size_t)phys * sc.Hkv + cur.kvh) * C::BLKB;
             uint8_t *dst = stg + (size_t)s * 2 * C::BLKB;
-            bulk_g2s(dst, kc + src, C::BLKB, &bars[s]);
-            bulk_g2s(dst + C::BLKB, vc + src, C::BLKB, &bars[s]);
+            if constexpr (C::W) {  // K and V are read once; the scores are to stay in L2
+                const uint64_t pol = l2_evict_first();
+                bulk_g2s_hint(dst, kc + src, C::BLKB, &bars[s], pol);
+                bulk_g2s_hint(dst + C::BLKB, vc + src, C::BLKB, &bars[s], pol);
+            } else {
+                bulk_g2s(dst, kc + src, C::BLKB, &bars[s]);
+                bulk_g2s(dst + C::BLKB, vc + src, C::BLKB, &bars[s]);
+            }
         }
         ++issued;
         ++j;

@@ -114,6 +114,12 @@ def _need(t, name, dtype=None, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _current(device):
+    """The call launches on the current device: its tensors must live there."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
@@ -329,6 +335,7 @@ def decode_tree(out, q, cu_q_lens, prefix_lens, mask, block_tables, k_cache, v_c
     MAX_TREE_ROWS drafts a sequence."""
     desc = _caches(k_cache, v_cache)
     dev = k_cache.device
+    _current(dev)
     _need(q, "q", torch.bfloat16, dev)
     _need(out, "out", torch.bfloat16, dev)
     _need(cu_q_lens, "cu_q_lens", torch.int32, dev)
@@ -380,6 +387,7 @@ def decode_weights(out, weights, q, k_cache, v_cache, block_tables, seq_lens, sc
     already; None: all of them)."""
     desc = _caches(k_cache, v_cache)
     dev = k_cache.device
+    _current(dev)
     _need(q, "q", torch.bfloat16, dev)
     _need(out, "out", torch.bfloat16, dev)
     _token_weights(weights, desc, dev)
@@ -409,6 +417,7 @@ def select_tokens(keep, keep_lens, weights, block_tables, seq_lens, num_sink, nu
     weights fp32 [num_blocks, Hkv, 16]."""
     _need(weights, "weights", torch.float32)
     dev = weights.device
+    _current(dev)
     _need(keep, "keep", torch.int32, dev)
     _need(keep_lens, "keep_lens", torch.int32, dev)
     _need(block_tables, "block_tables", torch.int32, dev)
@@ -434,6 +443,7 @@ def compact_kv(k_cache, v_cache, block_tables, keep, keep_lens, weights=None, st
     [B] (None: 0)."""
     desc = _caches(k_cache, v_cache)
     dev = k_cache.device
+    _current(dev)
     _need(block_tables, "block_tables", torch.int32, dev)
     _need(keep, "keep", torch.int32, dev)
     _need(keep_lens, "keep_lens", torch.int32, dev)

@@ -289,6 +289,36 @@ class KVManager:
             self.alloc.decref(b)
         seq.block_table = []
 
+    def make_private(self, seq: Sequence, first_pos: int = 0) -> None:
+        """Give ``seq`` blocks of its own for positions ``first_pos`` on:
+        every such block that other sequences share, or that the prefix
+        cache names, is replaced by a copy (emitted for ``pa_copy_blocks``).
+        Needed before ``pa_compact_kv`` moves tokens inside the sequence,
+        and before ``pa_decode_weights`` where sequences share blocks."""
+        cache = self.alloc.cache
+        for j in range(first_pos // BLOCK_SIZE, len(seq.block_table)):
+            b = seq.block_table[j]
+            if self.alloc.ref[b] > 1 or (cache is not None and cache.holds(b)):
+                d = self.alloc.alloc()
+                self.pending_copies.append((b, d))
+                self.alloc.copies_emitted += 1
+                self.alloc.decref(b)
+                seq.block_table[j] = d
+
+    def truncate(self, seq: Sequence, num_cached: int) -> None:
+        """Keep the first ``num_cached`` positions of ``seq`` and release the
+        blocks behind them: rejected drafts, or what a compaction left."""
+        if not 0 <= num_cached <= BLOCK_SIZE * len(seq.block_table):
+            raise ValueError(f"sequence {seq.seq_id} holds {len(seq.block_table)} blocks, not {num_cached} positions")
+        keep = blocks_for(num_cached)
+        for b in reversed(seq.block_table[keep:]):
+            self.alloc.decref(b)
+        del seq.block_table[keep:]
+        if not seq.in_prefill:
+            seq.prefill_end = num_cached
+            seq.num_tokens = num_cached + 1
+        seq.num_cached = num_cached
+
     def take_copies(self) -> np.ndarray:
         c = np.array(self.pending_copies, np.int32).reshape(-1, 2)
         self.pending_copies = []

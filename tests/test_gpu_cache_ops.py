@@ -173,6 +173,27 @@ def test_tree_bad_block(cuda_device):
     assert bool(((out.double() - ref).abs()[4:] <= tol[4:]).all())
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G", [1, 8])
+def test_tree_smallest(cuda_device, G, fp8):
+    """One draft of one sequence (fewer rows than a copy box), with and without a prefix."""
+    for prefix in (0, 1, 130):
+        check_tree(*make_tree(12 + prefix, [prefix], [1], 1, G, 64, fp8))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_many_long_segments(cuda_device, fp8):
+    """Segments cut at every place: two row tiles, one, and both in a sequence."""
+    check_tree(*make_tree(13, [3000, 700, 5, 1290, 2048], [64, 17, 33, 48, 16], 2, 8, 64, fp8))
+
+
+def test_calls_refuse_another_current_device(cuda_device, monkeypatch):
+    c, q, cu, pre, mask, scale = make_tree(14, [40], [4], 2, 2, 64)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        run_tree(c, q, cu, pre, mask, scale)
+
+
 # --------------------------------------------------------- attention weights
 def run_weights(c, q, lens, scale, w, seen):
     qd, kd = dev(q), dev(c.k)
@@ -485,6 +506,33 @@ def test_budgeted_serving(cuda_device):
                 assert U.same_bits(kd[int(c.tables[b, t // 16]), h, t % 16], newk[b * T + node, h])
                 assert U.same_bits(vd[int(c.tables[b, t // 16]), h, t % 16], newv[b * T + node, h])
     assert ops.get_last_device_error() == 0
+
+
+def test_compaction_beside_a_fork(cuda_device):
+    """A sequence that shares its blocks with another gets copies before its
+    tokens are moved; the other one's cache keeps its bits."""
+    from paged_kv_cache_408_b200.runtime import BlockAllocator, Scheduler, SchedulerConfig, check_invariants
+    Hkv, D = 2, 64
+    sc = Scheduler(BlockAllocator(24), SchedulerConfig(watermark=0.0))
+    a = sc.restore(0, 90, 8)
+    b = sc.fork(a, 1, 8)
+    g = torch.Generator().manual_seed(91)
+    k = torch.randn(24, Hkv, 16, D, generator=g).bfloat16()
+    kd, vd = dev(k).clone(), dev(k).clone()
+    sc.kv.make_private(b, 4)
+    pairs = torch.from_numpy(sc.kv.take_copies()).cuda()
+    ops.copy_blocks(kd, vd, pairs)
+    keep = torch.tensor([[[0, 1, 2, 3] + list(range(50, 90))]], dtype=torch.int32)
+    table = torch.tensor([b.block_table], dtype=torch.int32)
+    before = kd.cpu().clone()
+    ops.compact_kv(kd, vd, dev(table), dev(keep), torch.tensor([44], dtype=torch.int32).cuda())
+    sc.kv.truncate(b, 44)
+    assert ops.get_last_device_error() == 0 and len(b.block_table) == 3
+    want = U.compact_plain(before, table, keep.numpy(), [44], [0])
+    assert U.same_bits(kd, want) and U.same_bits(vd, want)
+    for x in a.block_table:
+        assert U.same_bits(kd[x], k[x])
+    check_invariants(sc)
 
 
 # ------------------------------------------------- streams, graphs, workspaces

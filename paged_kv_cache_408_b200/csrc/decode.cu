@@ -461,6 +461,14 @@ PA_DEVICE PieceAt piece_at(const DecodeArgs &a, const Item &it, size_t row0, int
     return {row0 * a.max_parts + it.piece + a.prefix_pieces, (size_t)a.max_parts};
 }
 
+// Log2-sum-exp of a piece with running maximum m and sum l.  For the attention
+// weights a NaN among the scores stays one: every weight of the row is then.
+template <class C>
+PA_DEVICE float piece_lse(float m, float l) {
+    if (C::W && l != l) return l;
+    return (l > 0.f) ? m + lg2(l) : -INFINITY;
+}
+
 // ---- tensor-core decode (fp8 cache, GQA groups of 8) ----------------------
 //
 // With an fp8 cache and 8 q heads per kv head, q.k and p.v on CUDA cores
@@ -699,8 +707,8 @@ PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &p
                 for (int i = 0; i < VB / 8; ++i) dst[i] = make_uint4(wds[4 * i], wds[4 * i + 1], wds[4 * i + 2], wds[4 * i + 3]);
             }
             if (C::W && r == 0) {
-                a.ws_row_lse[row0 + 2 * c] = (l0 > 0.f) ? m0 + lg2(l0) : -INFINITY;
-                a.ws_row_lse[row0 + 2 * c + 1] = (l1 > 0.f) ? m1 + lg2(l1) : -INFINITY;
+                a.ws_row_lse[row0 + 2 * c] = piece_lse<C>(m0, l0);
+                a.ws_row_lse[row0 + 2 * c + 1] = piece_lse<C>(m1, l1);
             }
             if (lane == 0 && a.ws_np) a.ws_np[(size_t)it.b * Hkv + it.kvh] = 1;
         } else {
@@ -721,8 +729,8 @@ PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &p
                 }
             }
             if (r == 0) {
-                a.ws_lse[at.base + 2 * c * at.stride] = (l0 > 0.f) ? m0 + lg2(l0) : -INFINITY;
-                a.ws_lse[at.base + (2 * c + 1) * at.stride] = (l1 > 0.f) ? m1 + lg2(l1) : -INFINITY;
+                a.ws_lse[at.base + 2 * c * at.stride] = piece_lse<C>(m0, l0);
+                a.ws_lse[at.base + (2 * c + 1) * at.stride] = piece_lse<C>(m1, l1);
             }
             if (lane == 0 && it.piece == 0) {
                 a.ws_np[(size_t)it.b * Hkv + it.kvh] = it.npieces + a.prefix_pieces;
@@ -1029,7 +1037,7 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                             *reinterpret_cast<uint4 *>(dst + choff[c] * 8) = make_uint4(wds[0], wds[1], wds[2], wds[3]);
                         }
                         if (C::W && sub == 0)
-                            a.ws_row_lse[row0 + h] = (l[h] > 0.f) ? m[h] + lg2(l[h]) : -INFINITY;
+                            a.ws_row_lse[row0 + h] = piece_lse<C>(m[h], l[h]);
                     }
                 }
                 if (lane == 0 && a.ws_np) a.ws_np[(size_t)it.b * Hkv + it.kvh] = 1;  // nothing to merge
@@ -1052,7 +1060,7 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                                                 acc2[h][4 * c + 3].x * inv, acc2[h][4 * c + 3].y * inv);
                         }
                         if (sub == 0)  // sub 0 has sh == 0: slot h is head h
-                            a.ws_lse[at.base + h * at.stride] = (l[h] > 0.f) ? m[h] + lg2(l[h]) : -INFINITY;
+                            a.ws_lse[at.base + h * at.stride] = piece_lse<C>(m[h], l[h]);
                     }
                 }
                 if (lane == 0 && it.piece == 0) {

@@ -308,8 +308,6 @@ PA_DEVICE void store_chunks(uint8_t *row, int u, int r, const uint32_t (&h)[8]) 
     }
 }
 
-PA_DEVICE bool not_finite(float x) { return !(fabsf(x) <= 3.4028235e38f); }
-
 // P.V multiplies the V rows of drafts that a row does not see by zero, and
 // zero times an infinity or a NaN is NaN.  So where a segment's drafts hold
 // one, its affected rows are attended again, by one warp with the formula
@@ -319,13 +317,25 @@ template <class C>
 __device__ __noinline__ bool drafts_not_finite(const TreeArgs &a, const Item &it, int lane) {
     bool bad = false;
 #pragma unroll 1
-    for (int t = it.P; t < it.L; ++t) {
+    for (int t = it.P + lane; t < it.L; t += 32) {  // a draft a lane
         const int64_t blk = a.block_tables[(size_t)it.b * a.max_blocks + (t >> 4)];
         if (blk < 0 || blk >= a.num_blocks) continue;
-        float v[C::D / 32];
-        load_dims<C::D, C::FP8>(a.v_cache, (blk * a.Hkv + it.kvh) * 16 + (t & 15), lane, v);
+        const int64_t row = (blk * a.Hkv + it.kvh) * 16 + (t & 15);
+        constexpr int E = C::FP8 ? 1 : 2;
+        const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.v_cache) + row * C::D * E);
 #pragma unroll
-        for (int e = 0; e < C::D / 32; ++e) bad |= not_finite(v[e]);
+        for (int i = 0; i < C::D * E / 16; ++i) {
+            const uint4 x = v[i];
+            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (C::FP8) {  // a code of seven ones
+                    bad |= (((wd[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                } else {  // an exponent of eight ones
+                    bad |= (wd[e] & 0x7f80u) == 0x7f80u || (wd[e] & 0x7f800000u) == 0x7f800000u;
+                }
+            }
+        }
     }
     return __any_sync(kFull, bad);
 }
@@ -752,7 +762,6 @@ __global__ void __launch_bounds__(C::NT, 1)
                     const int ch = D == 128 ? (u ^ (ct & 7)) : (u ^ ((ct >> 1) & 3));
                     src[u] = live ? *reinterpret_cast<const uint4 *>(codes + 16 * ch) : make_uint4(0, 0, 0, 0);
                 }
-                mbar_arrive(&cempty[cs]);
                 uint32_t nan = 0;
 #pragma unroll
                 for (int u = 0; u < D / 16; ++u) {
@@ -769,6 +778,9 @@ __global__ void __launch_bounds__(C::NT, 1)
                     }
                     store_chunks<C>(row, u, ct, h);
                 }
+                // only now, with every code used: an arrival straight behind
+                // the loads let the next copy overwrite codes still on their way
+                mbar_arrive(&cempty[cs]);
                 if (nan & 0x80808080u) {  // a NaN has no place in the scaled range: write it
 #pragma unroll 1
                     for (int d = 0; d < D; ++d) {

@@ -43,7 +43,7 @@ PA_DEVICE float row_lse(const float *lse, int first, int np, int lane) {
     for (int p = lane; p < np; p += 32) l += ex2(__ldcg(lse + (size_t)piece_slot(first, p) * G) - mb);
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    return l > 0.f ? mb + lg2(l) : INFINITY;  // no weight at all: 2^-inf = 0 for every token
+    return l > 0.f ? mb + lg2(l) : l == l ? INFINITY : l;  // no weight at all: 2^-inf = 0 for every token
 }
 
 template <int D, int G>

@@ -279,6 +279,24 @@ def test_weights_bad_metadata(cuda_device):
     assert ops.get_last_device_error() == ops.DEVERR_BAD_BLOCK
 
 
+@pytest.mark.parametrize("fp8,G", [(False, 4), (True, 2), (True, 8)])
+@pytest.mark.parametrize("n", [40, 3000])
+def test_weights_nan_key(cuda_device, fp8, G, n):
+    """A NaN in a key makes every weight of its sequence and kv head NaN, as
+    the softmax over it is, in one piece or in many; no other weight."""
+    c = U.paged(28, [n, n], 2, 64, fp8)
+    t = n // 2
+    c.k.view(torch.uint8 if fp8 else torch.int16)[int(c.tables[0, t // 16]), 1, t % 16, 3] = 0x7f if fp8 else 0x7fc0
+    q = torch.randn(2, 2 * G, 64).bfloat16()
+    out, w = run_weights(c, q, [n, n], 0.125, torch.zeros(c.k.shape[:3]), [0, 0])
+    tok = torch.arange(n)
+    for b in range(2):
+        for h in range(2):
+            bad = b == 0 and h == 1
+            assert bool((torch.isnan(w[c.tables[b].long()[tok // 16], h, tok % 16]) == bad).all())
+            assert bool((torch.isnan(out[b, h * G:(h + 1) * G]) == bad).all())
+
+
 # ------------------------------------------------------------------ selection
 def check_select(seed, lens, Hkv, budget, sink, recent, make=None, width=None):
     rng = np.random.RandomState(seed)
@@ -606,6 +624,27 @@ def test_two_streams_at_once(cuda_device):
     for a, (ref, tol) in zip(work, refs):
         assert bool(((a[0].cpu().double() - ref).abs() <= tol).all())
     assert ops.get_last_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_repeatable_under_load(cuda_device, fp8, D):
+    """Every SM busy with many tiles: the same bits from every call, and the
+    right ones (a tile overwritten too early shows here, not on a few tiles)."""
+    B, n, T, Hkv, G = 40, 1000, 36, 4, 8
+    c = U.paged(83, [n + T] * B, Hkv, D, fp8)
+    g = torch.Generator().manual_seed(84)
+    q = (torch.randn(B * T, Hkv * G, D, generator=g) * 1.5).bfloat16()
+    mask = U.tree_masks(85, [T] * B)
+    cu, prefix = [i * T for i in range(B + 1)], [n] * B
+    first = run_tree(c, q, cu, prefix, mask, 1 / math.sqrt(D))
+    for _ in range(4):
+        assert U.same_bits(run_tree(c, q, cu, prefix, mask, 1 / math.sqrt(D)), first)
+    for b in (0, 17, 39):
+        one = U.Paged(c.k, c.v, c.tables[b:b + 1], c.k_scale, c.v_scale)
+        rows = slice(b * T, (b + 1) * T)
+        ref, tol = U.tree64(one, q[rows], [0, T], [n], mask[rows], 1 / math.sqrt(D), 2.0 ** -11 if fp8 else 2.0 ** -8)
+        assert bool(((first[rows].double() - ref).abs() <= tol).all())
 
 
 def test_bitwise_repeatable(cuda_device):

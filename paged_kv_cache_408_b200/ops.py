@@ -312,6 +312,61 @@ def prefill_chunk(out, q, cu_q_lens, prefix_lens, block_tables, k_cache, v_cache
         _stream(stream)))
 
 
+# The calls below are short enough on the GPU (5-20 us) for the binding itself
+# to count: arguments are checked with one expression each, and go through the
+# full checks of _need, which say what is wrong, only where that fails.
+def _arg(t, name, dtype, index):
+    """Device pointer of a contiguous tensor of `dtype` on CUDA device `index`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        _need(t, name, dtype, torch.device("cuda", index))
+    return t.data_ptr()
+
+
+def _buffer(t, name, index):
+    """(pointer, bytes) of a workspace."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.is_contiguous()):
+        _need(t, name, None, torch.device("cuda", index))
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _device_index(t, name):
+    """The tensor's device, which has to be the current one."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _need(t, name)
+    _current(t.device)
+    return t.get_device()
+
+
+def _kv(k_cache, v_cache):
+    """(descriptor, device index, k pointer, v pointer)."""
+    index = _device_index(k_cache, "k_cache")
+    desc = cache_desc(k_cache)
+    if not k_cache.is_contiguous():
+        _need(k_cache, "k_cache")
+    v = _arg(v_cache, "v_cache", k_cache.dtype, index)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    return desc, index, k_cache.data_ptr(), v
+
+
+def _scale_args(desc, k_scale, v_scale, index):
+    if desc.dtype != DTYPE_FP8_E4M3:
+        return None, None
+    k_scale, v_scale = _scales(desc, k_scale, v_scale, torch.device("cuda", index))
+    return k_scale.data_ptr(), v_scale.data_ptr()
+
+
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _token_weights(weights, desc, index):
+    w = _arg(weights, "weights", torch.float32, index)
+    if weights.shape != (desc.num_blocks, desc.num_kv_heads, BLOCK_SIZE):
+        raise ValueError(f"weights must be [num_blocks, Hkv, {BLOCK_SIZE}], got {tuple(weights.shape)}")
+    return w
+
+
 def tree_workspace_size(num_seqs, num_q_heads, max_q_len, max_blocks_per_seq, k_cache) -> int:
     desc = cache_desc(k_cache)
     out = C.c_size_t(0)
@@ -333,35 +388,25 @@ def decode_tree(out, q, cu_q_lens, prefix_lens, mask, block_tables, k_cache, v_c
     prefix_lens int32 [n]; mask int64 (or uint64) [total_q], bit j = the row
     sees draft j of its sequence; block_tables int32 [n, max_blocks]; at most
     MAX_TREE_ROWS drafts a sequence."""
-    desc = _caches(k_cache, v_cache)
-    dev = k_cache.device
-    _current(dev)
-    _need(q, "q", torch.bfloat16, dev)
-    _need(out, "out", torch.bfloat16, dev)
-    _need(cu_q_lens, "cu_q_lens", torch.int32, dev)
-    _need(prefix_lens, "prefix_lens", torch.int32, dev)
-    _need(mask, "mask", (torch.int64, torch.uint64), dev)
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _need(workspace, "workspace", None, dev)
+    desc, dev, kp, vp = _kv(k_cache, v_cache)
+    qp, op = _arg(q, "q", torch.bfloat16, dev), _arg(out, "out", torch.bfloat16, dev)
+    cp, pp = _arg(cu_q_lens, "cu_q_lens", torch.int32, dev), _arg(prefix_lens, "prefix_lens", torch.int32, dev)
+    uint64 = isinstance(mask, torch.Tensor) and mask.dtype is torch.uint64
+    mp = _arg(mask, "mask", torch.uint64 if uint64 else torch.int64, dev)
+    tp = _arg(block_tables, "block_tables", torch.int32, dev)
+    wp, wn = _buffer(workspace, "workspace", dev)
     n = prefix_lens.numel()
     if cu_q_lens.numel() != n + 1 or block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("cu_q_lens must be [n+1], block_tables [n, max_blocks]")
     if q.dim() != 3 or out.shape != q.shape or q.shape[2] != desc.head_dim:
         raise ValueError("out/q shape mismatch")
     total, Hq, _ = q.shape
-    if mask.shape != (total,):
+    if mask.dim() != 1 or mask.shape[0] != total:
         raise ValueError("mask must be [total_q]")
-    ks, vs = _scales(desc, k_scale, v_scale, dev)
+    ks, vs = _scale_args(desc, k_scale, v_scale, dev)
     _check("pa_decode_tree", lib().pa_decode_tree(
-        _ptr(out), _ptr(q), _ptr(cu_q_lens), _ptr(prefix_lens), _ptr(mask), _ptr(block_tables), n,
-        block_tables.shape[1], Hq, int(max_q_len), total, _ptr(k_cache), _ptr(v_cache), float(scale), _ptr(ks),
-        _ptr(vs), _ptr(workspace), workspace.numel() * workspace.element_size(), C.byref(desc), _stream(stream)))
-
-
-def _token_weights(weights, desc, device):
-    _need(weights, "weights", torch.float32, device)
-    if weights.shape != (desc.num_blocks, desc.num_kv_heads, BLOCK_SIZE):
-        raise ValueError(f"weights must be [num_blocks, Hkv, {BLOCK_SIZE}], got {tuple(weights.shape)}")
+        op, qp, cp, pp, mp, tp, n, block_tables.shape[1], Hq, int(max_q_len), total, kp, vp, float(scale), ks, vs, wp, wn,
+        C.byref(desc), _raw_stream(stream, dev)))
 
 
 def weights_workspace_size(num_seqs, num_q_heads, max_blocks_per_seq, k_cache) -> int:
@@ -385,29 +430,25 @@ def decode_weights(out, weights, q, k_cache, v_cache, block_tables, seq_lens, sc
     weight, summed over its kv head's query heads, to weights fp32
     [num_blocks, Hkv, 16]; seen_lens int32 [B] (positions whose sum is there
     already; None: all of them)."""
-    desc = _caches(k_cache, v_cache)
-    dev = k_cache.device
-    _current(dev)
-    _need(q, "q", torch.bfloat16, dev)
-    _need(out, "out", torch.bfloat16, dev)
-    _token_weights(weights, desc, dev)
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
-    _need(workspace, "workspace", None, dev)
+    desc, dev, kp, vp = _kv(k_cache, v_cache)
+    qp, op = _arg(q, "q", torch.bfloat16, dev), _arg(out, "out", torch.bfloat16, dev)
+    tw = _token_weights(weights, desc, dev)
+    tp, lp = _arg(block_tables, "block_tables", torch.int32, dev), _arg(seq_lens, "seq_lens", torch.int32, dev)
+    wp, wn = _buffer(workspace, "workspace", dev)
     if q.dim() != 3 or out.shape != q.shape or q.shape[2] != desc.head_dim:
         raise ValueError("out/q shape mismatch")
     B, Hq, _ = q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
+    sp = None
     if seen_lens is not None:
-        _need(seen_lens, "seen_lens", torch.int32, dev)
+        sp = _arg(seen_lens, "seen_lens", torch.int32, dev)
         if seen_lens.shape != (B,):
             raise ValueError("seen_lens must be [B]")
-    ks, vs = _scales(desc, k_scale, v_scale, dev)
+    ks, vs = _scale_args(desc, k_scale, v_scale, dev)
     _check("pa_decode_weights", lib().pa_decode_weights(
-        _ptr(out), _ptr(weights), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens),
-        _ptr(seen_lens), B, block_tables.shape[1], Hq, float(scale), _ptr(ks), _ptr(vs), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), C.byref(desc), _stream(stream)))
+        op, tw, qp, kp, vp, tp, lp, sp, B, block_tables.shape[1], Hq, float(scale), ks, vs, wp, wn, C.byref(desc),
+        _raw_stream(stream, dev)))
 
 
 def select_tokens(keep, keep_lens, weights, block_tables, seq_lens, num_sink, num_recent, stream=None):
@@ -415,13 +456,10 @@ def select_tokens(keep, keep_lens, weights, block_tables, seq_lens, num_sink, nu
     (keep int32 [B, Hkv, budget], ascending, then -1; keep_lens int32 [B]):
     the first num_sink, the last num_recent, the heaviest of the rest by
     weights fp32 [num_blocks, Hkv, 16]."""
-    _need(weights, "weights", torch.float32)
-    dev = weights.device
-    _current(dev)
-    _need(keep, "keep", torch.int32, dev)
-    _need(keep_lens, "keep_lens", torch.int32, dev)
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
+    dev = _device_index(weights, "weights")
+    wp = _arg(weights, "weights", torch.float32, dev)
+    kp, np_ = _arg(keep, "keep", torch.int32, dev), _arg(keep_lens, "keep_lens", torch.int32, dev)
+    tp, lp = _arg(block_tables, "block_tables", torch.int32, dev), _arg(seq_lens, "seq_lens", torch.int32, dev)
     if weights.dim() != 3 or weights.shape[2] != BLOCK_SIZE:
         raise ValueError(f"weights must be [num_blocks, Hkv, {BLOCK_SIZE}], got {tuple(weights.shape)}")
     nb, hkv, bs = weights.shape
@@ -432,8 +470,8 @@ def select_tokens(keep, keep_lens, weights, block_tables, seq_lens, num_sink, nu
         raise ValueError("keep must be [B, Hkv, budget]")
     desc = CacheDesc(nb, hkv, bs, 128, DTYPE_BF16)  # the call reads num_blocks and num_kv_heads only
     _check("pa_select_tokens", lib().pa_select_tokens(
-        _ptr(keep), _ptr(keep_lens), _ptr(weights), _ptr(block_tables), _ptr(seq_lens), B, block_tables.shape[1],
-        keep.shape[2], int(num_sink), int(num_recent), C.byref(desc), _stream(stream)))
+        kp, np_, wp, tp, lp, B, block_tables.shape[1], keep.shape[2], int(num_sink), int(num_recent), C.byref(desc),
+        _raw_stream(stream, dev)))
 
 
 def compact_kv(k_cache, v_cache, block_tables, keep, keep_lens, weights=None, start_lens=None, stream=None):
@@ -441,26 +479,23 @@ def compact_kv(k_cache, v_cache, block_tables, keep, keep_lens, weights=None, st
     keep[b, head, i] move to position start_lens[b] + i, in place; keep int32
     [B, Hkv or 1, max_keep] ascending, keep_lens int32 [B], start_lens int32
     [B] (None: 0)."""
-    desc = _caches(k_cache, v_cache)
-    dev = k_cache.device
-    _current(dev)
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _need(keep, "keep", torch.int32, dev)
-    _need(keep_lens, "keep_lens", torch.int32, dev)
+    desc, dev, kp, vp = _kv(k_cache, v_cache)
+    tp = _arg(block_tables, "block_tables", torch.int32, dev)
+    lp, np_ = _arg(keep, "keep", torch.int32, dev), _arg(keep_lens, "keep_lens", torch.int32, dev)
     B = keep_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be [B, max_blocks]")
     if keep.dim() != 3 or keep.shape[0] != B:
         raise ValueError("keep must be [B, Hkv or 1, max_keep]")
-    if weights is not None:
-        _token_weights(weights, desc, dev)
+    wp = None if weights is None else _token_weights(weights, desc, dev)
+    sp = None
     if start_lens is not None:
-        _need(start_lens, "start_lens", torch.int32, dev)
+        sp = _arg(start_lens, "start_lens", torch.int32, dev)
         if start_lens.shape != (B,):
             raise ValueError("start_lens must be [B]")
     _check("pa_compact_kv", lib().pa_compact_kv(
-        _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(block_tables), _ptr(keep), _ptr(keep_lens),
-        _ptr(start_lens), B, block_tables.shape[1], keep.shape[1], keep.shape[2], C.byref(desc), _stream(stream)))
+        kp, vp, wp, tp, lp, np_, sp, B, block_tables.shape[1], keep.shape[1], keep.shape[2], C.byref(desc),
+        _raw_stream(stream, dev)))
 
 
 def get_last_device_error(stream=None) -> int:

@@ -25,17 +25,33 @@
 // threads).  A segment of two row tiles has one on each stream, sharing the K
 // and V tiles; of one row tile the streams take the key tiles in turn, and the
 // two accumulators are joined at the end.  A loader warp gathers K and V tiles
-// through the block table (2-D TMA boxes, 128-byte swizzle) into two rings;
-// one thread issues the MMAs, the scores of step n+1 before P.V of step n, so
-// that the tensor pipe works while the exponentials run.  P is written over
-// its scores in TMEM and is the A operand of P.V.  Warps whose 32 rows are all
-// past the drafts skip the arithmetic.
+// through the block table (TMA boxes, 128-byte swizzle) into two rings; one
+// thread issues the MMAs, the scores of step n+1 before P.V of step n, so that
+// the tensor pipe works while the exponentials run.  P is written over its
+// scores in TMEM and is the A operand of P.V, half a tile (64 keys) at a time.
+// Warps whose 32 rows are all past the drafts skip the arithmetic.
 // An E4M3 cache: the codes land in a staging ring and four warps widen them
-// to f16 operand tiles; the query rows are scaled by a power of two into
-// f16's range.
-// Bound: HBM for up to 128 rows a kv head (the tensor pipe then needs about
-// a third of the time that the K and V bytes take), the tensor and softmax
-// pipes beyond.
+// to f16 operand tiles; two more scale the query rows by a power of two into
+// f16's range.  f16 and not bf16 because every code is an f16 value and P
+// keeps three more bits.
+//
+// Bound (kernel alone, 8 kv heads, head_dim 128):
+//   16 x 32701 tokens, 32 drafts (128 rows a kv head): 350 us, 2.15 GB,
+//     6.15 TB/s, tensor pipe 42% -- HBM; called back to back for a second the
+//     1 kW power cap lowers the clock to 1.4 GHz and a call takes 430 us.
+//   64 x U[1,2048], 16 drafts: 68 us, 277 MB -- HBM and the segments: one of
+//     a single key tile takes 3.0 us against 1.45 us for a tile in a row
+//     (query tile, softmax, P.V and epilogue follow one another once).
+//   E4M3, 32 x U[1,8192], U[1,64] drafts of 64 heads: 260 us -- latency: no
+//     pipe is above 45% busy; a step's scores wait for the P.V that frees
+//     their columns, and 16 warps leave 128 registers a thread.
+// Measured and dropped: 64-key steps with two score buffers a stream (every
+// MMA N = 64; E4M3 64 drafts x 8000 tokens 794 against 702 us); a part of the
+// exponentials on the FMA pipe (797 against 771); a whole warp issuing the
+// MMAs in step, with votes after its waits (the same time); one pass over the
+// scores against the maximum so far, repeated where it moved (P of a
+// whole tile in registers: spills with an E4M3 cache); registers moved between warpgroups (the calls of the rare
+// path cannot be compiled so).
 #include <cudaTypedefs.h>
 
 #include <algorithm>

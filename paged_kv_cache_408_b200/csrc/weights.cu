@@ -13,11 +13,20 @@
 // again instead would cost D (2 D) bytes a token and kv head.  fp32, because
 // the sums that selection compares are fp32: a score rounded to f16 would
 // move a weight by up to |s| 2^-11.
+// K and V are read with the evict-first policy, so that the scores are still
+// in L2 when they are read back (E4M3 below: 143 -> 139 us).
 // The finishing kernel, a programmatic dependent, has for each (sequence, kv
 // head) CTAs that merge the pieces' outputs and, to add the weights, CTAs
-// that take a share of the tokens: the pieces' log2-sum-exps give
-// L_h, and each thread updates 4 tokens at a time (16 B of sums, 16 G B of
-// scores, loaded before L_h is known).
+// that take a share of the tokens: the pieces' log2-sum-exps give L_h, and
+// each thread updates 4 tokens at a time (16 B of sums, 16 G B of scores,
+// loaded before L_h is known).
+//
+// Bound: HBM.  64 sequences of U[1,2048] tokens, 8 kv heads of 4 x 128: 61 us
+// for 275 MB (57 us attending at 4.8 TB/s, as pa_decode does); E4M3, 8 x
+// 32768 tokens, groups of 8: 139 us for 554 MB (124 us attending: the
+// tensor-core path issues ~500 instructions a block and warp).  One sequence
+// of 700 tokens: 20 us, latency; shares down to 4 cost units over all SMs
+// took the attending from 42 us (pa_decode's smallest share is 16) to 14.
 #include <algorithm>
 
 #include "common.cuh"

@@ -352,8 +352,10 @@ int pa_decode_noalloc(void *out, const void *q, const void *k_cache, const void 
  *                 that share one must not overlap on the GPU.
  * A sequence whose lengths are out of range (more drafts than max_q_len,
  * rows past total_q_tokens, prefix + drafts past the block table) is flagged
- * PA_DEVERR_BAD_LEN and its rows are left as they are.  num_seqs in
- * [0, 2048]; num_kv_heads <= 128; num_q_heads / num_kv_heads in {1,2,4,8};
+ * PA_DEVERR_BAD_LEN and its rows are left as they are.  num_blocks *
+ * num_kv_heads * 16 must be below 2^31, and so must num_seqs * num_kv_heads *
+ * ceil(max_q_len * group / 256) * (7 + 3 * ceil(max_blocks_per_seq / 8)),
+ * else PA_ERR_UNSUPPORTED.  num_seqs in [0, 2048]; num_kv_heads <= 128; num_q_heads / num_kv_heads in {1,2,4,8};
  * head_dim 64 or 128; bf16 or fp8 E4M3 cache.  fp32 accumulation, rounded to
  * bf16 once at the end.
  */

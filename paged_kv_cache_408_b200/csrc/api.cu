@@ -276,7 +276,9 @@ int pa_decode_tree(void *out, const void *q, const int32_t *cu_q_lens, const int
         total_q_tokens > (int64_t)num_seqs * max_q_len || !(scale > 0.f) || scale > FLT_MAX)
         return PA_ERR_INVALID_ARG;
     // token rows are 32-bit coordinates of the tensor copies
-    if (desc->num_blocks > INT32_MAX / PA_BLOCK_SIZE / desc->num_kv_heads) return PA_ERR_UNSUPPORTED;
+    if (desc->num_blocks > INT32_MAX / PA_BLOCK_SIZE / desc->num_kv_heads ||
+        !pa::tree_fits(num_seqs, desc->num_kv_heads, num_q_heads / desc->num_kv_heads, max_q_len, max_blocks_per_seq))
+        return PA_ERR_UNSUPPORTED;
     const bool fp8 = desc->dtype == PA_DTYPE_FP8_E4M3;
     if (fp8 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
     if (total_q_tokens == 0) return PA_OK;

@@ -129,6 +129,12 @@ cudaError_t launch_decode_scores(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t st);
 // Tree attention of drafted tokens (tree.cu).
 constexpr int kMaxTreeRows = 64;  // drafts of a sequence: the bits of a row's mask
+// Whether the line of cost units that the batch is cut along fits 32 bits, for
+// tables of this width (at most 7 units a segment of up to 256 rows and 3 a
+// tile of 128 keys).
+inline bool tree_fits(int B, int Hkv, int G, int max_q_len, int max_blocks) {
+    return (int64_t)B * Hkv * ((max_q_len * G + 255) / 256) * (7 + 3 * (int64_t)((max_blocks + 7) / 8)) <= INT32_MAX;
+}
 size_t tree_ws_bytes(int D);
 cudaError_t launch_tree(const TreeArgs &a, void *workspace, cudaStream_t st);
 // Decode that also adds every cached token's attention weight to a running

@@ -121,6 +121,7 @@ struct TCfg {
     // E4M3: P is kept 2^7 times larger, so that f16 holds weights down to
     // 2^-31 of the largest (and up to 2^(7 + 8) before the maximum moves)
     static constexpr float PBIAS = FP8 ? 7.f : 0.f;
+    static_assert(SEG <= 7 && kPair <= 3, "tree_fits() counts on it");
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(COL_O + 2 * D <= 512, "TMEM columns");
     static_assert(NSK + 3 < NBAD && NST / 2 + NSK + 3 < NBAD, "bad-block ring");
@@ -1184,10 +1185,9 @@ cudaError_t run_tree(const TreeArgs &a, const TreeWs &ws, cudaStream_t st) {
              tiled_map(&tq, bf16, 3, a.q, qdims, qstrides, qbox, swz);
     }
     if (!ok) return cudaErrorInvalidValue;
-    // a CTA per SM, fewer where the batch has fewer key tiles; the most line units the batch can have, with tables of this width
+    // a CTA per SM, fewer where the batch has fewer key tiles
     const long long groups = (a.max_q_len + 2 * C::QPOS - 1) / (2 * C::QPOS);
     const long long tiles_wide = (a.max_blocks + C::BPT - 1) / C::BPT;
-    if ((long long)a.B * a.Hkv * groups * (C::SEG + kPair * tiles_wide) > INT32_MAX) return cudaErrorNotSupported;
     const int ctas = (int)std::min<long long>({(long long)a.B * a.Hkv * groups * tiles_wide, sm_count(), kMaxCtas});
     e = launch_pdl(tree_kernel<C>, dim3(ctas), dim3(C::NT), C::SMEM, st, a, ws, tk, tv, tq);
     if (e != cudaSuccess) return e;

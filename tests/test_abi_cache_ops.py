@@ -39,6 +39,8 @@ def test_tree_refusals():
         assert tree(scale=s) == INVALID
     assert tree(desc(dt=1)) == INVALID                   # fp8 needs its scales
     assert tree(ptr=None) == INVALID and tree(mask=None) == INVALID and tree(ptr=ODD) == INVALID
+    assert tree(desc(nb=(1 << 31) // 16 // 8 + 1)) == UNSUPPORTED  # token rows past 32 bits
+    assert tree(B=2048, maxb=1 << 20) == UNSUPPORTED     # a line of work past 32 bits
     assert tree(total=0) == 0                            # nothing to do
     assert tree(B=0, total=0) == 0
 

@@ -164,13 +164,40 @@ def test_tree_bad_metadata(cuda_device):
     assert ops.get_last_device_error() == ops.DEVERR_BAD_LEN and bool((out[2:] == 7).all())
 
 
-def test_tree_bad_block(cuda_device):
-    c, q, cu, pre, mask, scale = make_tree(11, [40, 50], [4, 4], 2, 2, 64)
-    c.tables[0, 1] = 10 ** 6
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tree_bad_block(cuda_device, D, fp8):
+    """A bad table entry is flagged and its keys are absent, as if they were not there."""
+    c, q, cu, pre, mask, scale = make_tree(11, [400, 50], [4, 4], 2, 2, D, fp8)
+    bad = [5, 24]                                    # prefix tokens 80..95, 384..399
+    c.tables[0, bad[0]], c.tables[0, bad[1]] = 10 ** 6, -1
+    ops.get_last_device_error()
     out = run_tree(c, q, cu, pre, mask, scale)
     assert ops.get_last_device_error() == ops.DEVERR_BAD_BLOCK
-    ref, tol = U.tree64(U.Paged(c.k, c.v, c.tables.clamp(max=c.k.shape[0] - 1)), q, cu, pre, mask, scale, 2.0 ** -8)
+    ok = U.Paged(c.k, c.v, c.tables.clamp(0, c.k.shape[0] - 1), c.k_scale, c.v_scale)
+    ref, tol = U.tree64(ok, q, cu, pre, mask, scale, 2.0 ** -8)
     assert bool(((out.double() - ref).abs()[4:] <= tol[4:]).all())
+    k, v = ok.rows64("k", 0, 404), ok.rows64("v", 0, 404)
+    for i in range(4):
+        see = torch.tensor([t // 16 not in bad for t in range(400)] + [bool((int(mask[i]) >> j) & 1) for j in range(4)])
+        for h in range(4):
+            o, _, av, dot = U.attend64(q[i, h].double(), k[:, h // 2], v[:, h // 2], scale, see)
+            assert bool(((out[i, h].double() - o).abs() <=
+                         2.0 ** -8 * o.abs() + (2.0 ** -8 + U.score_slack(D, dot)) * av).all())
+
+
+def test_tree_most_sequences(cuda_device):
+    """2048 sequences, most of them without drafts."""
+    rng = np.random.RandomState(15)
+    sizes = (rng.randint(0, 6, 2048) // 5 * rng.randint(1, 4, 2048)).tolist()
+    check_tree(*make_tree(15, rng.randint(0, 30, 2048).tolist(), sizes, 1, 2, 64))
+
+
+def test_tree_no_drafts_at_all(cuda_device):
+    """Rows behind the last sequence only: nothing is written."""
+    c, q, cu, pre, mask, scale = make_tree(16, [20, 3], [0, 0], 1, 2, 64)
+    out = run_tree(c, q, cu, pre, mask, scale, max_q=2, pad_rows=3)
+    assert bool((out == 7.0).all()) and ops.get_last_device_error() == 0
 
 
 @pytest.mark.parametrize("fp8", [False, True])

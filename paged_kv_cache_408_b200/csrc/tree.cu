@@ -115,6 +115,11 @@ struct TCfg {
     // 64 x 100 tokens take 3.0 us a segment of one tile against 1.45 us a tile
     // (bf16), 8 against 2 us (E4M3)
     static constexpr int SEG = FP8 ? 7 : 5;
+    // the next item's first K tile before this one's last V tile, or behind
+    // it: widening K takes as long as a softmax, so E4M3 wants it early (64 x
+    // 1000 tokens, 16 drafts: 102 against 108 us); a bf16 tile is only a copy
+    // (64 x U[1,2048], 16 drafts: 72 against 69)
+    static constexpr bool ACROSS = FP8;
     static constexpr uint32_t COL_O = 2 * KT;
     static constexpr uint32_t KV_ARRIVALS = FP8 ? NWIDEN * 32 : 1, Q_ARRIVALS = FP8 ? 64 : 1;  // that fill a tile
     static constexpr float OPMUL = FP8 ? 256.f : 1.f;  // E4M3: K and V operands are 2^-8 of their value (widen4)
@@ -264,6 +269,19 @@ PA_DEVICE bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+// Has phase `parity` of `bar` completed?  (Does not suspend the thread.)
+PA_DEVICE bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // The 16 rows of a block (two groups of 8, from group `g`): columns, rows,
@@ -513,8 +531,8 @@ __global__ void __launch_bounds__(C::NT, 1)
     };
     Item it;
     if (w == C::W_LOAD) {
-        // ---- K tile n+1, then V tile n (the order of their use), across the
-        // items of the share; a window of 32 block-table entries in registers
+        // ---- K tile j+1, then V tile j (the order of their use); a window of
+        // 32 block-table entries in registers
         const int32_t *bt = nullptr;
         int win0 = 0, went = 0, nblk = 0;
         auto tile_row = [&](const Item &i, int j, int n) {  // lanes 0..7: cache row of the tile's block
@@ -567,22 +585,35 @@ __global__ void __launch_bounds__(C::NT, 1)
             __syncwarp();
             return true;
         };
-        int n = 0, vrow = 0;
+        // the next item's first window is requested before this one's tiles
+        auto first_window = [&](const Item &i) {
+            return a.block_tables[(size_t)i.b * a.max_blocks + min(i.j0 * C::BPT + lane, ((i.L + 15) >> 4) - 1)];
+        };
+        Item nx;
+        bool more = walk.next(a, nx);
+        int nwent = more ? first_window(nx) : 0, n = 0, vrow = 0;
 #pragma unroll 1
-        while (ok && walk.next(a, it)) {
+        while (ok && more) {
+            it = nx;
+            went = nwent;
             bt = a.block_tables + (size_t)it.b * a.max_blocks;
             nblk = (it.L + 15) >> 4;
-            win0 = it.j0 * C::BPT - 32;  // (refilled by the first tile)
+            win0 = it.j0 * C::BPT;
+            more = walk.next(a, nx);
+            if (more) nwent = first_window(nx);
 #pragma unroll 1
-            for (int j = it.j0; j < it.j1 && ok; ++j, ++n) {
-                const int row = tile_row(it, j, n);
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv)
-                    if ((kv == 0 || n > 0) && !fill(kv, kv ? vrow : row)) break;
+            for (int j = it.j0; j < it.j1 + (C::ACROSS ? 0 : 1) && ok; ++j) {
+                const bool v = C::ACROSS ? n > 0 : j > it.j0;
+                int row = 0;
+                if (j < it.j1) {
+                    row = tile_row(it, j, n++);
+                    if (!fill(0, row)) break;
+                }
+                if (v && !fill(1, vrow)) break;
                 vrow = row;
             }
         }
-        if (ok && n > 0) fill(1, vrow);
+        if (C::ACROSS && ok && n > 0) fill(1, vrow);
         if (!ok) {  // the last copy of every slot may be in flight: wait for it, with a short fresh budget
             const uint64_t dd = drain_deadline();
             auto drain = [&](uint64_t *full, int ns, int issued) {
@@ -661,9 +692,11 @@ __global__ void __launch_bounds__(C::NT, 1)
                 for (int k = 0; k < steps && ok; ++k, ++n) {
                     const int qt = pair & k, qslot = (qc + qt) & 1;
                     // the scores first, so that the tensor pipe has them while
-                    // P(n-1) is computed; but where a new query tile takes the
-                    // place of one that the last scores read, P.V first
-                    const bool pv_first = k == 0 && (pair || was_pair);
+                    // P(n-1) is computed; but P.V first where a new query tile
+                    // takes the place of one that the last scores read, or a
+                    // new segment's operands have not landed
+                    const bool pv_first = k == 0 && (pair || was_pair || !mbar_test(&kfull[kr.slot], kr.phase) ||
+                                                     !mbar_test(&qfull[qslot], (qc >> 1) & 1));
                     if (pv_first && n > 0) pv();
                     if (k <= pair) wait(&qfull[qslot], ((qc + qt) >> 1) & 1);
                     scores(qslot, !pair || qt, k >= steps - 1 - pair);
@@ -763,7 +796,7 @@ __global__ void __launch_bounds__(C::NT, 1)
             // ---- E4M3: thread ct widens key row ct of each staged tile into its
             // f16 operand tile
             const int ct = tid - C::W_WIDEN * 32;
-            int kn = 0, vn = 0, cn = 0, n = 0, vkv0 = 0, vL = 0;
+            int kn = 0, vn = 0, cn = 0, n = 0;
             auto widen = [&](int kv, int kv0, int L, int nn) {
                 const int ns = kv ? NSV : NSK, m = kv ? vn : kn, sl = m % ns, cs = cn % NST;
                 if (!wait(&cfull[cs], (cn / NST) & 1)) return false;
@@ -810,6 +843,7 @@ __global__ void __launch_bounds__(C::NT, 1)
                 mbar_arrive((kv ? vfull : kfull) + sl);
                 return true;
             };
+            int vkv0 = 0, vL = 0;
             bool more = true;
 #pragma unroll 1
             while (ok && more) {  // K tile n+1 before V tile n, as the loader; at the end the last V tile alone
@@ -826,6 +860,7 @@ __global__ void __launch_bounds__(C::NT, 1)
                     ++n;
                 }
             }
+            static_assert(C::ACROSS, "the order of this loop");
         }
     } else {
         // ---- softmax: warpgroup g takes the steps n with n % 2 == g; thread

@@ -25,8 +25,8 @@
 // for 275 MB (57 us attending at 4.8 TB/s, as pa_decode does); E4M3, 8 x
 // 32768 tokens, groups of 8: 139 us for 554 MB (124 us attending: the
 // tensor-core path issues ~500 instructions a block and warp).  One sequence
-// of 700 tokens: 20 us, latency; shares down to 4 cost units over all SMs
-// took the attending from 42 us (pa_decode's smallest share is 16) to 14.
+// of 700 tokens: 20 us, latency; shares down to 2 cost units over all SMs
+// took the attending from 42 us (pa_decode's smallest share is 16) to 12.
 #include <algorithm>
 
 #include "common.cuh"

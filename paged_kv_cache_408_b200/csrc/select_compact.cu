@@ -70,6 +70,15 @@ PA_DEVICE void cluster_sync() {
     __syncwarp();  // the aligned forms are executed by whole warps
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of cluster_sync().
+PA_DEVICE void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+PA_DEVICE void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // One 32-bit word of CTA `rank`'s shared memory, at the place of `p` in this CTA's.
 PA_DEVICE int dsmem_load(const int *p, uint32_t rank) {
     uint32_t a;
@@ -133,7 +142,7 @@ template <int THREADS>
 struct SelectSmem {
     alignas(16) int hist[3][kBins];
     int warp_a[THREADS / 32], warp_b[THREADS / 32];
-    int digit, above;      // digit of the k-th key in this pass; keys above it
+    int digit, above, count;  // digit of the k-th key in this pass; keys above it; keys that have it
     int cta_a, cta_b;      // this CTA's counts, read by the cluster
 };
 
@@ -192,28 +201,40 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     const int nquad = (n + 3) >> 2, per = (nquad + C - 1) / C;
     const int q0 = min(nquad, rank * per), q1 = min(nquad, q0 + per);
     const int32_t *bt = a.block_tables + (size_t)b * a.max_blocks;
-    auto load_quad = [&](int q) {  // the keys of tokens 4q .. 4q+3
+    // the keys of tokens 4q .. 4q+3; 0, which no weight has, for those that are
+    // not candidates
+    auto load_quad = [&](int q) {
         const int64_t blk = bt[q >> 2];
         float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (blk < 0 || blk >= a.num_blocks) flag_error(a.err, PA_DEVERR_BAD_BLOCK);
         else f = *reinterpret_cast<const float4 *>(a.weights + (blk * a.Hkv + h) * 16 + (q & 3) * 4);
-        return make_uint4(order_key(f.x), order_key(f.y), order_key(f.z), order_key(f.w));
+        uint4 u = make_uint4(order_key(f.x), order_key(f.y), order_key(f.z), order_key(f.w));
+        const int t = 4 * q;
+        if (t < lo || t + 4 > hi) {
+            if (t < lo || t >= hi) u.x = 0;
+            if (t + 1 < lo || t + 1 >= hi) u.y = 0;
+            if (t + 2 < lo || t + 2 >= hi) u.z = 0;
+            if (t + 3 < lo || t + 3 >= hi) u.w = 0;
+        }
+        return u;
     };
     auto quad = [&](int q) {  // the same, from shared memory where it is kept
         const int i = q - q0;
         return i < kSelCap / 4 ? reinterpret_cast<const uint4 *>(keys)[i] : load_quad(q);
     };
-    __syncthreads();  // the histograms are zero
+    if (C > 1) cluster_arrive();  // (waited for before the first remote add: that CTA has zeroed its bins, too)
+    __syncthreads();              // the histograms are zero
     for (int q = q0 + tid; q < q1; q += kSelThreads) {
         const uint4 u = load_quad(q);
         if (q - q0 < kSelCap / 4) reinterpret_cast<uint4 *>(keys)[q - q0] = u;
         const uint32_t e[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-            if (4 * q + x >= lo && 4 * q + x < hi) atomicAdd(&sm.hist[0][e[x] >> 21], 1);
+            if (e[x]) atomicAdd(&sm.hist[0][e[x] >> 21], 1);
     }
 
-    // ---- the k-th largest key, 11, 11 and 10 bits at a time
+    // ---- the k-th largest key, 11, 11 and 10 bits at a time; or, as soon as
+    // every key with the current prefix is to be taken, the one below them
     uint32_t prefix = 0;
     int need = k;  // keys still to take among those with the current prefix
 #pragma unroll 1
@@ -226,12 +247,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
                 const uint32_t e[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    if ((e[x] >> above_shift) == (prefix >> above_shift) && 4 * q + x >= lo && 4 * q + x < hi)
+                    if (e[x] && (e[x] >> above_shift) == (prefix >> above_shift))
                         atomicAdd(&sm.hist[pass][(e[x] >> shift) & mask], 1);
             }
         }
         __syncthreads();
         if (C > 1) {  // add this CTA's bins to the first CTA's
+            if (pass == 0) cluster_wait();
             if (rank > 0)
                 for (int i = tid; i < kBins; i += kSelThreads)
                     if (sm.hist[pass][i]) dsmem_add(&sm.hist[pass][i], 0, sm.hist[pass][i]);
@@ -252,14 +274,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
             if (above < need && above + bin[x] >= need) {
                 sm.digit = d0 + x;
                 sm.above = above;
+                sm.count = bin[x];
             }
             above += bin[x];
         }
         __syncthreads();
         prefix |= (uint32_t)sm.digit << shift;
         need -= sm.above;
+        if (need == sm.count) {  // (uniform over the cluster)
+            --prefix;
+            need = 0;
+            break;
+        }
         __syncthreads();
     }
+    __syncthreads();
 
     // ---- the places: warp w counts its contiguous part of the CTA's quads,
     // then walks it again with the counts of everything before it
@@ -272,9 +301,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
         const uint32_t e[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const bool in = 4 * q + x >= lo && 4 * q + x < hi;
-            gt += in && e[x] > kth;
-            eq += in && e[x] == kth;
+            gt += e[x] > kth;
+            eq += e[x] == kth;  // (kth is a weight's key or, with need 0, whatever is below one)
         }
     }
     gt = __reduce_add_sync(kFullMask, gt);
@@ -306,7 +334,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     for (int qb = wq0; qb < wq1; qb += 32) {
         const int q = qb + lane;
         uint32_t e[4] = {0, 0, 0, 0};
-        bool in[4];
         if (q < wq1) {
             const uint4 u = quad(q);
             e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
@@ -314,9 +341,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
         int g = 0, t = 0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            in[x] = q < wq1 && 4 * q + x >= lo && 4 * q + x < hi;
-            g += in[x] && e[x] > kth;
-            t += in[x] && e[x] == kth;
+            g += e[x] > kth;
+            t += e[x] == kth;
         }
         // both counts of a lane are at most 4: scan them packed
         int pk = g | (t << 16);
@@ -330,7 +356,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
         int gb = gbefore + (ex & 0xffff), eb = ebefore + (ex >> 16);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            if (!in[x]) continue;
             const bool isg = e[x] > kth, ise = e[x] == kth;
             if (isg || (ise && eb < need)) keep[a.sink + gb + min(eb, need)] = 4 * q + x;
             gb += isg;

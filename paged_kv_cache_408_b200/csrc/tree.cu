@@ -36,13 +36,13 @@
 // keeps three more bits.
 //
 // Bound (kernel alone, 8 kv heads, head_dim 128):
-//   16 x 32701 tokens, 32 drafts (128 rows a kv head): 350 us, 2.15 GB,
-//     6.15 TB/s, tensor pipe 42% -- HBM; called back to back for a second the
-//     1 kW power cap lowers the clock to 1.4 GHz and a call takes 430 us.
-//   64 x U[1,2048], 16 drafts: 68 us, 277 MB -- HBM and the segments: one of
+//   16 x 32701 tokens, 32 drafts (128 rows a kv head): 334 us, 2.15 GB,
+//     6.4 TB/s, tensor pipe 45% -- HBM; called back to back for a second the
+//     1 kW power cap lowers the clock to 1.3 GHz and a call takes 410 us.
+//   64 x U[1,2048], 16 drafts: 66 us, 277 MB -- HBM and the segments: one of
 //     a single key tile takes 3.0 us against 1.45 us for a tile in a row
 //     (query tile, softmax, P.V and epilogue follow one another once).
-//   E4M3, 32 x U[1,8192], U[1,64] drafts of 64 heads: 260 us -- latency: no
+//   E4M3, 32 x U[1,8192], U[1,64] drafts of 64 heads: 269 us -- latency: no
 //     pipe is above 45% busy; a step's scores wait for the P.V that frees
 //     their columns, and 16 warps leave 128 registers a thread.
 // Measured and dropped: 64-key steps with two score buffers a stream (every

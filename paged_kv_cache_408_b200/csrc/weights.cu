@@ -23,9 +23,9 @@
 //
 // Bound: HBM.  64 sequences of U[1,2048] tokens, 8 kv heads of 4 x 128: 61 us
 // for 275 MB (57 us attending at 4.8 TB/s, as pa_decode does); E4M3, 8 x
-// 32768 tokens, groups of 8: 139 us for 554 MB (124 us attending: the
+// 32768 tokens, groups of 8: 140 us for 554 MB (126 us attending: the
 // tensor-core path issues ~500 instructions a block and warp).  One sequence
-// of 700 tokens: 20 us, latency; shares down to 2 cost units over all SMs
+// of 700 tokens: 12.5 us in a graph, latency; shares down to 2 cost units over all SMs
 // took the attending from 42 us (pa_decode's smallest share is 16) to 12.
 #include <algorithm>
 

@@ -1109,50 +1109,76 @@ __global__ void __launch_bounds__(C::NT, 1)
 
 // Log-sum-exp merge of the cut segment that begins in CTA blockIdx.x: piece 0
 // in its slot 2 g + 1, the others in slot 2 (g + p) of the CTAs after it.
-// One warp per row.
+// One warp per row.  The first pieces' sums and outputs are requested together
+// with the description (their places do not depend on it, and every slot is
+// there to be read), so a segment of up to kMergeAhead pieces costs one round
+// trip.
+constexpr int kMergeAhead = 3;
+
 template <int D, int G>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a, const TreeWs ws, int ctas) {
     constexpr int E = D / 32;
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, g = blockIdx.x;
-    const int4 d = ws.desc[g];
-    const int np = d.w;
-    if (np < 1 || g + np > ctas) return;
+    auto load = [&](size_t at, float (&v)[E]) {
+        const float *src = ws.o + at * D + lane * E;
+        if constexpr (E == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+            v[0] = x.x, v[1] = x.y;
+        }
+    };
+    const int4 d = __ldcg(ws.desc + g);
 #pragma unroll 1
-    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < d.y; r += gridDim.y * 4) {
+    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < 256; r += gridDim.y * 4) {
         auto at = [&](int p) { return (size_t)(2 * (g + p) + (p == 0 ? 1 : 0)) * 256 + r; };
+        float lse[kMergeAhead], o[kMergeAhead][E];
+#pragma unroll
+        for (int p = 0; p < kMergeAhead; ++p) {
+            lse[p] = __ldcg(ws.lse + at(p));
+            load(at(p), o[p]);
+        }
+        const int np = d.w;
+        if (np < 1 || g + np > ctas || r >= d.y) return;
         float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-        for (int p = lane; p < np; p += 32) m = fmaxf(m, __ldcg(ws.lse + at(p)));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        for (int p = 0; p < kMergeAhead; ++p)
+            if (p < np) m = fmaxf(m, lse[p]);
+        if (np > kMergeAhead) {
+#pragma unroll 1
+            for (int p = kMergeAhead + lane; p < np; p += 32) m = fmaxf(m, __ldcg(ws.lse + at(p)));
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+        }
         const float mb = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-        for (int p = lane; p < np; p += 32) l += ex2(__ldcg(ws.lse + at(p)) - mb);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-        const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
         float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int p = 0; p < np; ++p) {
-            const float lp = __ldcg(ws.lse + at(p)), wt = ex2(lp - mb) * inv;
-            const float *src = ws.o + at(p) * D + lane * E;
+        // a piece without weight (none of its keys is visible) adds nothing
+        auto add = [&](float lp, const float (&v)[E]) {
+            const float wt = ex2(lp - mb);
+            l += wt;
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + e));
-                // a piece without weight (none of its keys is visible) adds nothing
-                acc[e] = lp == -INFINITY ? acc[e] : fmaf(wt, v.x, acc[e]);
-                acc[e + 1] = lp == -INFINITY ? acc[e + 1] : fmaf(wt, v.y, acc[e + 1]);
-            }
+            for (int e = 0; e < E; ++e) acc[e] = lp == -INFINITY ? acc[e] : fmaf(wt, v[e], acc[e]);
+        };
+#pragma unroll
+        for (int p = 0; p < kMergeAhead; ++p)
+            if (p < np) add(lse[p], o[p]);
+#pragma unroll 4
+        for (int p = kMergeAhead; p < np; ++p) {
+            float v[E];
+            load(at(p), v);
+            add(__ldcg(ws.lse + at(p)), v);
         }
+        const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
                              ((size_t)(d.x + r / G) * a.Hq + (size_t)d.z * G + r % G) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(acc[e], acc[e + 1]);
+            *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
     }
 }
 
@@ -1223,7 +1249,8 @@ cudaError_t run_tree(const TreeArgs &a, const TreeWs &ws, cudaStream_t st) {
     // a CTA per SM, fewer where the batch has fewer key tiles
     const long long groups = (a.max_q_len + 2 * C::QPOS - 1) / (2 * C::QPOS);
     const long long tiles_wide = (a.max_blocks + C::BPT - 1) / C::BPT;
-    const int ctas = (int)std::min<long long>({(long long)a.B * a.Hkv * groups * tiles_wide, sm_count(), kMaxCtas});
+    const int ctas = (int)std::min<long long>({(long long)a.B * a.Hkv * groups * tiles_wide, sm_count(),
+                                                kMaxCtas - kMergeAhead});  // (the merge looks that far past the last)
     e = launch_pdl(tree_kernel<C>, dim3(ctas), dim3(C::NT), C::SMEM, st, a, ws, tk, tv, tq);
     if (e != cudaSuccess) return e;
     return launch_pdl(tree_merge_kernel<C::D, C::G>, dim3(ctas, 32), dim3(128), 0, st, a, ws, ctas);

@@ -580,6 +580,41 @@ def test_compaction_beside_a_fork(cuda_device):
     check_invariants(sc)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_blocks_past_32_bit_offsets(cuda_device, fp8):
+    """A pool whose elements (and, with E4M3, bytes) pass 2^31: the same bits
+    from its last blocks as from a small pool."""
+    Hkv, G, D, n, T = 8, 4, 128, 300, 5
+    c, q, cu, prefix, mask, scale = make_tree(95, [n], [T], Hkv, G, D, fp8)
+    small = c.k.shape[0]
+    big = (1 << 31) // (Hkv * 16 * D) + 64 + small
+    raw = lambda x: x.view(torch.uint8) if fp8 else x
+    pools = []
+    for x in (c.k, c.v):
+        y = torch.zeros(big, Hkv, 16, D, dtype=raw(x).dtype, device="cuda")
+        y[big - small:] = raw(x).cuda()
+        pools.append(y.view(x.dtype))
+    high = torch.where(c.tables >= 0, c.tables + (big - small), c.tables)
+    h = U.Paged(pools[0], pools[1], high, c.k_scale, c.v_scale)
+    assert U.same_bits(run_tree(h, q, cu, prefix, mask, scale), run_tree(c, q, cu, prefix, mask, scale))
+    w = torch.rand(c.k.shape[:3])
+    wh = torch.zeros(big, Hkv, 16)
+    wh[big - small:] = w
+    a, b = run_weights(c, q[:1], [n], scale, w, [n - 1]), run_weights(h, q[:1], [n], scale, wh, [n - 1])
+    assert U.same_bits(a[0], b[0]) and U.same_bits(a[1], b[1][big - small:])
+    keep = torch.zeros(2, 1, Hkv, 100, dtype=torch.int32, device="cuda")
+    kl = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    ops.select_tokens(keep[0], kl[0], dev(a[1]), dev(c.tables), lens, 4, 20)
+    ops.select_tokens(keep[1], kl[1], dev(b[1]), dev(high), lens, 4, 20)
+    assert torch.equal(keep[0], keep[1])
+    kk, vv = dev(c.k).clone(), dev(c.v).clone()
+    ops.compact_kv(kk, vv, dev(c.tables), keep[0], kl[0])
+    ops.compact_kv(pools[0], pools[1], dev(high), keep[1], kl[1])
+    assert U.same_bits(pools[0][big - small:], kk) and U.same_bits(pools[1][big - small:], vv)
+    assert ops.get_last_device_error() == 0
+
+
 # ------------------------------------------------- streams, graphs, workspaces
 def test_calls_in_a_graph_on_another_stream(cuda_device):
     """All four calls captured into one graph on a side stream and replayed

@@ -745,40 +745,40 @@ __global__ void __launch_bounds__(C::NT, 1)
                     const int ch = lane % LPR, at = ch / 8, cc = ch % 8;
 #pragma unroll 1
                     for (int rb = (w - C::W_QUERY) * 64 + lane / LPR; rb < (w - C::W_QUERY + 1) * 64; rb += 8 * RPW) {
-                    uint4 v[8];  // 8 rows' loads in flight
+                        uint4 v[8];  // 8 rows' loads in flight
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int r = rb + u * RPW;
-                        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
-                                                   ((size_t)(q0 + r / G) * a.Hq + (size_t)it.kvh * G + r % G) * D + ch * 8;
-                        v[u] = r < nrows ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int r = rb + u * RPW;
-                        const uint32_t wd[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                        float2 f[4];
-                        float amax = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            f[e] = bf16x2_to_float2(wd[e]);
-                            amax = fmax3(amax, fabsf(f[e].x), fabsf(f[e].y));
+                        for (int u = 0; u < 8; ++u) {
+                            const int r = rb + u * RPW;
+                            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
+                                                       ((size_t)(q0 + r / G) * a.Hq + (size_t)it.kvh * G + r % G) * D + ch * 8;
+                            v[u] = r < nrows ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
-                        for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-                        int ex = 0;
-                        if (amax > 0.f) ex = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xff) - 127), -100), 100);
-                        const float qs = __uint_as_float((uint32_t)(127 + ex) << 23);
-                        uint32_t h[4];
+                        for (int u = 0; u < 8; ++u) {
+                            const int r = rb + u * RPW;
+                            const uint32_t wd[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                            float2 f[4];
+                            float amax = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __half2 hh = __floats2half2_rn(f[e].x * qs, f[e].y * qs);
-                            h[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                            for (int e = 0; e < 4; ++e) {
+                                f[e] = bf16x2_to_float2(wd[e]);
+                                amax = fmax3(amax, fabsf(f[e].x), fabsf(f[e].y));
+                            }
+#pragma unroll
+                            for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+                            int ex = 0;
+                            if (amax > 0.f) ex = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xff) - 127), -100), 100);
+                            const float qs = __uint_as_float((uint32_t)(127 + ex) << 23);
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __half2 hh = __floats2half2_rn(f[e].x * qs, f[e].y * qs);
+                                h[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                            }
+                            *reinterpret_cast<uint4 *>(tile + at * C::ATOM + r * 128 + ((cc ^ (r & 7)) * 16)) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
+                            if (ch == 0) qexp[(qc & 3) * 128 + r] = (int8_t)ex;
                         }
-                        *reinterpret_cast<uint4 *>(tile + at * C::ATOM + r * 128 + ((cc ^ (r & 7)) * 16)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                        if (ch == 0) qexp[(qc & 3) * 128 + r] = (int8_t)ex;
-                    }
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(&qfull[sl]);

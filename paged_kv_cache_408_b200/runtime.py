@@ -62,6 +62,7 @@ class BlockAllocator:
         if sorted(self.free_list) != list(range(self.num_blocks)):
             raise ValueError("order must be a permutation of the pool")
         self.ref = np.zeros(self.num_blocks, np.int32)
+        self.pins: dict[int, int] = {}  # blocks that copies still to run read or write -> how many of them
         self.copies_emitted = 0
         self.cache: PrefixCache | None = None  # attached by PrefixCache
 
@@ -90,11 +91,26 @@ class BlockAllocator:
         if self.ref[b] <= 0:
             raise RuntimeError(f"decref of free block {b}")
         self.ref[b] -= 1
-        if self.ref[b] == 0:
-            if self.cache is not None and self.cache.holds(b):
-                self.cache.park(b)  # stays cached until a lookup revives it or space is needed
-            else:
-                self.free_list.append(b)
+        if self.ref[b] == 0 and b not in self.pins:
+            self._give_back(b)
+
+    def _give_back(self, b: int) -> None:
+        if self.cache is not None and self.cache.holds(b):
+            self.cache.park(b)  # stays cached until a lookup revives it or space is needed
+        else:
+            self.free_list.append(b)
+
+    def pin(self, b: int) -> None:
+        """Keep ``b`` from being handed out, even when its last reference
+        goes, until as many ``unpin`` calls."""
+        self.pins[b] = self.pins.get(b, 0) + 1
+
+    def unpin(self, b: int) -> None:
+        self.pins[b] -= 1
+        if self.pins[b] == 0:
+            del self.pins[b]
+            if self.ref[b] == 0:
+                self._give_back(b)
 
 
 # ------------------------------------------------------------ prefix cache
@@ -165,7 +181,7 @@ class PrefixCache:
             parent = b
         for b in blocks:
             if self.alloc.ref[b] == 0:
-                del self.lru[b]
+                self.lru.pop(b, None)  # (a pinned block is not parked yet)
                 self.alloc.ref[b] = 1
             else:
                 self.alloc.incref(b)
@@ -266,13 +282,20 @@ class KVManager:
             raise RuntimeError("positions must be written in order")
         b = seq.block_table[j]
         if self.alloc.ref[b] > 1:  # shared: copy before the first divergent write
-            d = self.alloc.alloc()
-            self.pending_copies.append((b, d))
-            self.alloc.copies_emitted += 1
-            self.alloc.decref(b)
-            seq.block_table[j] = d
-            b = d
+            b = self._copy_block(seq, j)
         return b * BLOCK_SIZE + off
+
+    def _copy_block(self, seq: Sequence, j: int) -> int:
+        """Replace block j of ``seq`` by a copy of its own.  The pairs of one
+        list are copied at the same time, so the source, which may have no
+        holder left, is nobody else's until ``take_copies``."""
+        b, d = seq.block_table[j], self.alloc.alloc()
+        self.pending_copies.append((b, d))
+        self.alloc.copies_emitted += 1
+        self.alloc.pin(b)
+        self.alloc.decref(b)
+        seq.block_table[j] = d
+        return d
 
     def fork(self, parent: Sequence, seq_id: int, decode_left: int) -> Sequence:
         child = Sequence(seq_id, parent.num_tokens, decode_left, parent.num_cached, parent.prefill_end,
@@ -299,11 +322,7 @@ class KVManager:
         for j in range(first_pos // BLOCK_SIZE, len(seq.block_table)):
             b = seq.block_table[j]
             if self.alloc.ref[b] > 1 or (cache is not None and cache.holds(b)):
-                d = self.alloc.alloc()
-                self.pending_copies.append((b, d))
-                self.alloc.copies_emitted += 1
-                self.alloc.decref(b)
-                seq.block_table[j] = d
+                self._copy_block(seq, j)
 
     def truncate(self, seq: Sequence, num_cached: int) -> None:
         """Keep the first ``num_cached`` positions of ``seq`` and release the
@@ -320,7 +339,11 @@ class KVManager:
         seq.num_cached = num_cached
 
     def take_copies(self) -> np.ndarray:
+        """The pairs recorded so far.  They must have run (in stream order)
+        before anything that is planned after this call."""
         c = np.array(self.pending_copies, np.int32).reshape(-1, 2)
+        for b, _ in self.pending_copies:
+            self.alloc.unpin(b)
         self.pending_copies = []
         return c
 
@@ -605,7 +628,8 @@ class Scheduler:
 # ------------------------------------------------------------ invariants
 def check_invariants(sched: Scheduler) -> None:
     """refcount[p] == number of block tables referencing p; the free list,
-    the parked cached blocks and the referenced blocks partition the pool;
+    the parked cached blocks, the referenced blocks and those that only a
+    pending copy keeps partition the pool;
     every cached key names a block that is referenced or parked, and its
     parent is cached too."""
     a = sched.alloc
@@ -627,11 +651,13 @@ def check_invariants(sched: Scheduler) -> None:
     if a.cache is not None:
         parked[list(a.cache.lru)] = True
         for b, key in a.cache.key_of.items():
-            if free[b] or (a.ref[b] == 0 and not parked[b]):
+            if free[b] or (a.ref[b] == 0 and not parked[b] and b not in a.pins):
                 raise AssertionError(f"cached block {b} is free")
             if a.cache.block_of.get(key) != b or (key[0] >= 0 and key[0] not in a.cache.key_of):
                 raise AssertionError(f"cache maps of block {b} disagree")
         if any(b not in a.cache.key_of for b in a.cache.lru):
             raise AssertionError("a parked block has no key")
-    if np.any(free & parked) or np.any((free | parked) & (a.ref > 0)) or np.any(~(free | parked) & (a.ref == 0)):
-        raise AssertionError("free list, parked cached blocks and referenced blocks do not partition the pool")
+    held = a.ref > 0
+    held[list(a.pins)] = True
+    if np.any(free & parked) or np.any((free | parked) & held) or np.any(~(free | parked) & ~held):
+        raise AssertionError("free list, parked cached blocks and held blocks do not partition the pool")

@@ -1,0 +1,74 @@
+"""Copy lists of the block manager: the pairs of one list are copied at the
+same time, so no destination may be a source or another pair's destination,
+however full the pool is."""
+import numpy as np
+import pytest
+
+from paged_kv_cache_408_b200.runtime import (BlockAllocator, KVManager, OutOfBlocksError, PrefixCache, Scheduler,
+                                             SchedulerConfig, Sequence, check_invariants)
+
+
+def cached_sequence(blocks, tokens):
+    """A sequence whose full blocks the prefix cache names, in a pool of `blocks`."""
+    alloc = BlockAllocator(blocks)
+    cache, kv = PrefixCache(alloc), KVManager(alloc)
+    s = Sequence(0, tokens, 4, tokens, tokens, False, [alloc.alloc() for _ in range((tokens + 15) // 16)])
+    cache.insert(np.arange(tokens), s.block_table)
+    return alloc, cache, kv, s
+
+
+def check_pairs(pairs):
+    src, dst = [p[0] for p in pairs], [p[1] for p in pairs]
+    assert len(set(dst)) == len(dst), f"two copies into one block: {pairs}"
+    assert not set(src) & set(dst), f"a block is read and written by one list: {pairs}"
+
+
+def test_private_blocks_of_a_full_pool_leave_sources_alone():
+    """The one free block is taken; the first source, which only the prefix
+    cache still names, must not become the second copy's destination."""
+    alloc, cache, kv, s = cached_sequence(4, 40)
+    named = s.block_table[:2]
+    with pytest.raises(OutOfBlocksError):
+        kv.make_private(s)
+    pairs = kv.take_copies().tolist()
+    check_pairs(pairs)
+    assert pairs == [[named[0], s.block_table[0]]]
+    kv.make_private(s)                           # that copy is on its way: its source can be evicted now
+    check_pairs(kv.take_copies().tolist())
+    assert not any(cache.holds(b) for b in s.block_table)
+
+
+def test_sources_stay_cached_until_the_copies_are_taken():
+    alloc, cache, kv, s = cached_sequence(6, 40)
+    named = s.block_table[:2]
+    kv.make_private(s)
+    assert alloc.num_free == 1                   # the sources are not to be had yet
+    other = [alloc.alloc()]
+    with pytest.raises(OutOfBlocksError):
+        alloc.alloc()
+    n, blocks = cache.match(np.arange(40))       # but a lookup finds them
+    assert n == 32 and blocks == named
+    pairs = kv.take_copies().tolist()
+    check_pairs(pairs)
+    assert [p[0] for p in pairs] == named
+    for b in blocks + other:
+        alloc.decref(b)
+    assert alloc.num_free == 3
+
+
+def test_a_source_whose_last_holder_leaves_is_not_handed_out():
+    """A fork copies a shared block; the other holder retires before the copy
+    has run."""
+    sc = Scheduler(BlockAllocator(3), SchedulerConfig(watermark=0.0))
+    a = sc.restore(0, 10, 4)
+    b = sc.fork(a, 1, 4)
+    x = a.block_table[0]
+    sc.kv.slot_for(b, 10)
+    sc.retire(a)
+    check_invariants(sc)
+    c = sc.restore(2, 10, 4)
+    assert c.block_table != [x]
+    check_invariants(sc)
+    check_pairs(sc.kv.take_copies().tolist())
+    assert sc.alloc.num_free == 1
+    check_invariants(sc)

@@ -267,7 +267,7 @@ class KVManager:
 
     def __init__(self, allocator: BlockAllocator):
         self.alloc = allocator
-        self.pending_copies: list[tuple[int, int]] = []
+        self.pending_copies: dict[int, int] = {}  # destination -> source
 
     def slot_for(self, seq: Sequence, pos: int) -> int:
         """Slot of position ``pos`` (must be seq.num_cached + k for the
@@ -287,15 +287,26 @@ class KVManager:
 
     def _copy_block(self, seq: Sequence, j: int) -> int:
         """Replace block j of ``seq`` by a copy of its own.  The pairs of one
-        list are copied at the same time, so the source, which may have no
-        holder left, is nobody else's until ``take_copies``."""
+        list are copied at the same time, so source and destination, which
+        may have no holder left, are nobody else's until ``take_copies``."""
         b, d = seq.block_table[j], self.alloc.alloc()
-        self.pending_copies.append((b, d))
+        self.pending_copies[d] = b
         self.alloc.copies_emitted += 1
         self.alloc.pin(b)
+        self.alloc.pin(d)
         self.alloc.decref(b)
         seq.block_table[j] = d
         return d
+
+    def _drop_block(self, b: int) -> None:
+        """One holder of ``b`` less; a copy into it that nobody will read is
+        taken off the list, which frees both of its blocks."""
+        cache = self.alloc.cache
+        if b in self.pending_copies and self.alloc.ref[b] == 1 and not (cache is not None and cache.holds(b)):
+            self.alloc.unpin(self.pending_copies.pop(b))
+            self.alloc.unpin(b)
+            self.alloc.copies_emitted -= 1
+        self.alloc.decref(b)
 
     def fork(self, parent: Sequence, seq_id: int, decode_left: int) -> Sequence:
         child = Sequence(seq_id, parent.num_tokens, decode_left, parent.num_cached, parent.prefill_end,
@@ -309,7 +320,7 @@ class KVManager:
         # first, so that its LRU evicts a prefix's leaves before its root
         order = seq.block_table if self.alloc.cache is None else reversed(seq.block_table)
         for b in order:
-            self.alloc.decref(b)
+            self._drop_block(b)
         seq.block_table = []
 
     def make_private(self, seq: Sequence, first_pos: int = 0) -> None:
@@ -331,7 +342,7 @@ class KVManager:
             raise ValueError(f"sequence {seq.seq_id} holds {len(seq.block_table)} blocks, not {num_cached} positions")
         keep = blocks_for(num_cached)
         for b in reversed(seq.block_table[keep:]):
-            self.alloc.decref(b)
+            self._drop_block(b)
         del seq.block_table[keep:]
         if not seq.in_prefill:
             seq.prefill_end = num_cached
@@ -341,10 +352,11 @@ class KVManager:
     def take_copies(self) -> np.ndarray:
         """The pairs recorded so far.  They must have run (in stream order)
         before anything that is planned after this call."""
-        c = np.array(self.pending_copies, np.int32).reshape(-1, 2)
-        for b, _ in self.pending_copies:
+        c = np.array([(b, d) for d, b in self.pending_copies.items()], np.int32).reshape(-1, 2)
+        for d, b in self.pending_copies.items():
             self.alloc.unpin(b)
-        self.pending_copies = []
+            self.alloc.unpin(d)
+        self.pending_copies = {}
         return c
 
 

@@ -72,3 +72,53 @@ def test_a_source_whose_last_holder_leaves_is_not_handed_out():
     check_pairs(sc.kv.take_copies().tolist())
     assert sc.alloc.num_free == 1
     check_invariants(sc)
+
+
+def test_a_copy_whose_destination_is_given_back_is_dropped():
+    """make_private, truncate, make_private before the copies are taken: the
+    block that comes back is the destination of one copy, not of two."""
+    sc = Scheduler(BlockAllocator(5), SchedulerConfig(watermark=0.0))
+    a = sc.restore(0, 16, 4)
+    x = sc.restore(1, 16, 4)
+    b, y = sc.fork(a, 2, 4), sc.fork(x, 3, 4)
+    free = sc.alloc.num_free
+    sc.kv.make_private(b)
+    sc.kv.truncate(b, 0)
+    check_invariants(sc)
+    assert sc.alloc.num_free == free and not sc.alloc.pins
+    sc.kv.make_private(y)
+    pairs = sc.kv.take_copies().tolist()
+    check_pairs(pairs)
+    assert pairs == [[x.block_table[0], y.block_table[0]]]
+    check_invariants(sc)
+
+
+def test_a_copy_whose_sequence_ends_is_dropped():
+    sc = Scheduler(BlockAllocator(8), SchedulerConfig(watermark=0.0))
+    a = sc.restore(0, 40, 4)
+    b = sc.fork(a, 1, 4)
+    sc.kv.make_private(b, 20)
+    sc.retire(b)
+    sc.retire(a)
+    assert sc.kv.take_copies().size == 0 and sc.alloc.num_free == 8 and sc.alloc.copies_emitted == 0
+    check_invariants(sc)
+
+
+def test_a_destination_that_others_still_hold_is_copied():
+    """A destination that a fork holds, or that the prefix cache names, is not
+    dropped with its first sequence, nor handed out again before its copy."""
+    alloc, cache, kv, s = cached_sequence(5, 16)
+    kv.make_private(s)
+    t = kv.fork(s, 1, 4)
+    (d,) = s.block_table
+    kv.release(s)
+    assert list(kv.pending_copies) == [d]
+    cache.insert(np.arange(100, 116), [d])
+    kv.release(t)
+    for _ in range(3):
+        assert alloc.alloc() != d
+    with pytest.raises(OutOfBlocksError):        # the source and the destination wait for the copy
+        alloc.alloc()
+    check_pairs(kv.take_copies().tolist())
+    n, blocks = cache.match(np.arange(100, 116))
+    assert blocks == [d]

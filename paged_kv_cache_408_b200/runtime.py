@@ -290,9 +290,10 @@ class KVManager:
         list are copied at the same time, so source and destination, which
         may have no holder left, are nobody else's until ``take_copies``."""
         b, d = seq.block_table[j], self.alloc.alloc()
-        self.pending_copies[d] = b
+        src = self.pending_copies.get(b, b)  # a block that is itself still to be copied: from where it comes
+        self.pending_copies[d] = src
         self.alloc.copies_emitted += 1
-        self.alloc.pin(b)
+        self.alloc.pin(src)
         self.alloc.pin(d)
         self.alloc.decref(b)
         seq.block_table[j] = d

@@ -122,3 +122,18 @@ def test_a_destination_that_others_still_hold_is_copied():
     check_pairs(kv.take_copies().tolist())
     n, blocks = cache.match(np.arange(100, 116))
     assert blocks == [d]
+
+
+def test_a_copy_of_a_block_still_to_be_copied_comes_from_its_source():
+    """A private copy is forked and copied again before the first copy ran."""
+    sc = Scheduler(BlockAllocator(6), SchedulerConfig(watermark=0.0))
+    a = sc.restore(0, 16, 4)
+    b = sc.fork(a, 1, 4)
+    sc.kv.make_private(b)
+    c = sc.fork(b, 2, 4)
+    sc.kv.make_private(c)
+    (x,), (y,), (z,) = a.block_table, b.block_table, c.block_table
+    pairs = sc.kv.take_copies().tolist()
+    check_pairs(pairs)
+    assert pairs == [[x, y], [x, z]]
+    check_invariants(sc)

@@ -272,7 +272,9 @@ class KVManager:
     def slot_for(self, seq: Sequence, pos: int) -> int:
         """Slot of position ``pos`` (must be seq.num_cached + k for the
         positions being written this step, in order); allocates a block when
-        ``pos`` starts one and copies a shared block before writing into it."""
+        ``pos`` starts one and copies a block before writing into it that
+        other sequences share or that (behind a truncation) the prefix cache
+        names."""
         j, off = divmod(pos, BLOCK_SIZE)
         if j == len(seq.block_table):
             if off != 0:
@@ -281,9 +283,13 @@ class KVManager:
         elif j > len(seq.block_table):
             raise RuntimeError("positions must be written in order")
         b = seq.block_table[j]
-        if self.alloc.ref[b] > 1:  # shared: copy before the first divergent write
+        if self._shared(b):  # copy before the first divergent write
             b = self._copy_block(seq, j)
         return b * BLOCK_SIZE + off
+
+    def _shared(self, b: int) -> bool:
+        """Whether what lies in ``b`` is not one sequence's alone."""
+        return self.alloc.ref[b] > 1 or (self.alloc.cache is not None and self.alloc.cache.holds(b))
 
     def _copy_block(self, seq: Sequence, j: int) -> int:
         """Replace block j of ``seq`` by a copy of its own.  The pairs of one
@@ -330,10 +336,8 @@ class KVManager:
         cache names, is replaced by a copy (emitted for ``pa_copy_blocks``).
         Needed before ``pa_compact_kv`` moves tokens inside the sequence,
         and before ``pa_decode_weights`` where sequences share blocks."""
-        cache = self.alloc.cache
         for j in range(first_pos // BLOCK_SIZE, len(seq.block_table)):
-            b = seq.block_table[j]
-            if self.alloc.ref[b] > 1 or (cache is not None and cache.holds(b)):
+            if self._shared(seq.block_table[j]):
                 self._copy_block(seq, j)
 
     def truncate(self, seq: Sequence, num_cached: int) -> None:

@@ -137,3 +137,87 @@ def test_a_copy_of_a_block_still_to_be_copied_comes_from_its_source():
     check_pairs(pairs)
     assert pairs == [[x, y], [x, z]]
     check_invariants(sc)
+
+
+def test_writing_behind_a_truncation_leaves_a_cached_block_alone():
+    """A truncation can end inside a block that the prefix cache names; the
+    next token goes into a copy, a later prompt still finds the original."""
+    alloc, cache, kv, s = cached_sequence(8, 48)
+    named = list(s.block_table)
+    kv.truncate(s, 20)
+    slot = kv.slot_for(s, 20)
+    assert slot // 16 == s.block_table[1] != named[1] and slot % 16 == 4
+    assert kv.take_copies().tolist() == [[named[1], s.block_table[1]]]
+    n, blocks = cache.match(np.arange(48))
+    assert n == 48 and blocks == named
+    slot = kv.slot_for(s, 21)                    # its own now
+    assert slot == s.block_table[1] * 16 + 5 and kv.take_copies().size == 0
+
+
+def test_random_histories_keep_lists_pool_and_contents_sound():
+    """Forks, private copies, truncations, retirements, appends and cached
+    prefixes in any order, the copies run now and then, under a pool that is
+    often full: every list can be copied at once, and every sequence's blocks
+    hold its own tokens."""
+    for seed in range(80):
+        rng = np.random.default_rng(seed)
+        sc = Scheduler(BlockAllocator(int(rng.integers(4, 24))), SchedulerConfig(watermark=0.0, prefix_cache=seed % 2 == 0))
+        mem = np.full((sc.alloc.num_blocks, 16), -1)
+        text, nxt, token = {}, 0, 0
+
+        def run_copies():
+            pairs = sc.kv.take_copies()
+            check_pairs(pairs.tolist())
+            if len(pairs):
+                mem[pairs[:, 1]] = mem[pairs[:, 0]]
+
+        for _ in range(200):
+            op = rng.integers(0, 7)
+            s = sc.running[int(rng.integers(0, len(sc.running)))] if sc.running else None
+            try:
+                if op == 0 or s is None:
+                    n = int(rng.integers(1, 60))
+                    if (n + 15) // 16 > sc.alloc.num_free:
+                        continue
+                    s = sc.restore(nxt, n, 4)
+                    text[nxt] = list(range(token, token + n))
+                    run_copies()
+                    for i, t in enumerate(text[nxt]):
+                        mem[s.block_table[i // 16], i % 16] = t
+                    nxt, token = nxt + 1, token + n
+                elif op == 1:
+                    sc.fork(s, nxt, 4)
+                    text[nxt] = list(text[s.seq_id])
+                    nxt += 1
+                elif op == 2:
+                    sc.kv.make_private(s, int(rng.integers(0, 40)))
+                elif op == 3:
+                    n = int(rng.integers(0, s.num_cached + 1))
+                    sc.kv.truncate(s, n)
+                    del text[s.seq_id][n:]
+                elif op == 4:
+                    sc.retire(s)
+                elif op == 5:
+                    slot = sc.kv.slot_for(s, s.num_cached)
+                    run_copies()
+                    mem[slot // 16, slot % 16] = token
+                    text[s.seq_id].append(token)
+                    token += 1
+                    s.num_cached += 1
+                    s.prefill_end = s.num_cached
+                elif sc.cache is not None:
+                    sc.cache.insert(text[s.seq_id], s.block_table)
+            except OutOfBlocksError:
+                pass
+            if rng.random() < 0.2:
+                run_copies()
+                for s in sc.running:
+                    assert [mem[s.block_table[i // 16], i % 16] for i in range(s.num_cached)] == text[s.seq_id]
+                if sc.cache is not None:
+                    for s in sc.running:
+                        n, blocks = sc.cache.match(text[s.seq_id])
+                        got = [int(t) for x in blocks for t in mem[x]]
+                        assert got == text[s.seq_id][:n]
+                        for x in blocks:
+                            sc.alloc.decref(x)
+            check_invariants(sc)

@@ -239,6 +239,9 @@ class Sequence:
     num_cached   positions whose K/V are in the cache;
     prefill_end  positions that must be cached before decoding resumes;
     decode_left  decode steps still to run (a synthetic stop length);
+    num_dropped  tokens whose K/V a compaction took out: the sequence's text
+                 is num_cached + num_dropped tokens long so far, its cache and
+                 table hold num_cached;
     """
     seq_id: int
     num_tokens: int
@@ -251,6 +254,7 @@ class Sequence:
     admitted_at: int = -1
     preemptions: int = 0
     tokens: np.ndarray | None = None  # prompt token ids (needed only for prefix caching)
+    num_dropped: int = 0
 
     @property
     def in_prefill(self) -> bool:
@@ -317,7 +321,7 @@ class KVManager:
 
     def fork(self, parent: Sequence, seq_id: int, decode_left: int) -> Sequence:
         child = Sequence(seq_id, parent.num_tokens, decode_left, parent.num_cached, parent.prefill_end,
-                         parent.fresh, list(parent.block_table), parent.status)
+                         parent.fresh, list(parent.block_table), parent.status, num_dropped=parent.num_dropped)
         for b in child.block_table:
             self.alloc.incref(b)
         return child
@@ -340,9 +344,25 @@ class KVManager:
             if self._shared(seq.block_table[j]):
                 self._copy_block(seq, j)
 
+    def compacted(self, seq: Sequence, num_cached: int) -> None:
+        """``pa_compact_kv`` has moved ``num_cached`` tokens that a selection
+        kept to the front of ``seq``: the others' are gone from the cache, not
+        from the sequence's text.  (A preemption recomputes the whole text.)
+        Releases the blocks behind them."""
+        if not 0 <= num_cached <= seq.num_cached:
+            raise ValueError(f"sequence {seq.seq_id} has {seq.num_cached} cached positions, not {num_cached} to keep")
+        gone = seq.num_cached - num_cached
+        seq.num_dropped += gone
+        if seq.in_prefill:  # as many positions are still to come
+            seq.prefill_end -= gone
+            seq.num_cached = num_cached
+        self.truncate(seq, num_cached)
+
     def truncate(self, seq: Sequence, num_cached: int) -> None:
-        """Keep the first ``num_cached`` positions of ``seq`` and release the
-        blocks behind them: rejected drafts, or what a compaction left."""
+        """The text of ``seq`` ends behind its first ``num_cached`` positions
+        (rejected drafts, a step back): release the blocks behind them.  Not
+        for what a selection left, which is no beginning of the text: see
+        ``compacted``."""
         if not 0 <= num_cached <= BLOCK_SIZE * len(seq.block_table):
             raise ValueError(f"sequence {seq.seq_id} holds {len(seq.block_table)} blocks, not {num_cached} positions")
         keep = blocks_for(num_cached)
@@ -351,7 +371,7 @@ class KVManager:
         del seq.block_table[keep:]
         if not seq.in_prefill:
             seq.prefill_end = num_cached
-            seq.num_tokens = num_cached + 1
+            seq.num_tokens = num_cached + seq.num_dropped + 1
         seq.num_cached = num_cached
 
     def take_copies(self) -> np.ndarray:
@@ -479,15 +499,26 @@ class Scheduler:
         self.finished.append(seq)
 
     # -- policy pieces
-    def _preempt_one(self, plan: StepPlan) -> Sequence | None:
-        """Evict the most recently admitted running sequence (recompute)."""
-        if not self.running:
+    def _can_recompute(self, seq: Sequence) -> bool:
+        """Whether the whole text can be cached again: that of a compacted
+        sequence may have outgrown its table or the pool."""
+        need = blocks_for(max(seq.prefill_end, seq.num_cached) + seq.num_dropped + 1)
+        return not seq.num_dropped or need <= min(self.cfg.max_blocks_per_seq,
+                                                  self.alloc.num_blocks - self.watermark_blocks)
+
+    def _preempt_one(self, plan: StepPlan, oldest: Sequence) -> Sequence | None:
+        """Evict the most recently admitted running sequence (recompute), but
+        none admitted before ``oldest``, whose turn it is: those have their
+        slots of this step already.  A compacted sequence comes back with its
+        whole text, for the caller to compact again."""
+        victim = max((s for s in self.running if s.admitted_at >= oldest.admitted_at and self._can_recompute(s)),
+                     key=lambda s: s.admitted_at, default=None)
+        if victim is None:
             return None
-        victim = max(self.running, key=lambda s: s.admitted_at)
         self.running.remove(victim)
         self.kv.release(victim)
-        victim.prefill_end = victim.num_cached if not victim.in_prefill else victim.prefill_end
-        victim.num_cached = 0
+        victim.prefill_end = (victim.num_cached if not victim.in_prefill else victim.prefill_end) + victim.num_dropped
+        victim.num_cached = victim.num_dropped = 0
         victim.status = WAITING
         victim.preemptions += 1
         self.num_preemptions += 1
@@ -528,6 +559,7 @@ class Scheduler:
         # 2. decode first: one new token per decoding sequence
         decode: list[Sequence] = []
         slots: list[int] = []
+        waiting_for_blocks = False  # a sequence that cannot give way itself
         for s in sorted([s for s in self.running if not s.in_prefill], key=lambda s: s.admitted_at):
             if s.status != RUNNING:
                 continue  # preempted while making room for an earlier one
@@ -536,9 +568,10 @@ class Scheduler:
                     slot = self.kv.slot_for(s, s.num_cached)
                     break
                 except OutOfBlocksError:
-                    victim = self._preempt_one(plan)
+                    victim = self._preempt_one(plan, s)
                     if victim is None or victim is s:
                         slot = None
+                        waiting_for_blocks |= victim is None
                         break
             if slot is None:
                 continue
@@ -570,6 +603,8 @@ class Scheduler:
             if got:
                 chunks.append((s, s.num_cached, got))
                 budget -= got
+        if waiting_for_blocks and not (decode or chunks or plan.preempted):
+            raise OutOfBlocksError("compacted sequences too long to be recomputed hold the pool: none can go on")
         # 4. metadata
         plan.copies = self.kv.take_copies()
         plan.slots = np.array(slots, np.int64)
@@ -607,7 +642,7 @@ class Scheduler:
                 continue
             s.num_cached += 1
             s.prefill_end = s.num_cached
-            s.num_tokens = s.num_cached + 1
+            s.num_tokens = s.num_cached + s.num_dropped + 1
             s.decode_left -= 1
             if s.num_cached >= cap:  # the block table is full: the sequence ends here
                 s.decode_left = 0
@@ -617,8 +652,8 @@ class Scheduler:
             s.num_cached = start + n
             if s.num_cached >= s.prefill_end and s.fresh:
                 s.fresh = False
-                s.num_tokens = s.num_cached + 1  # the prompt's last position samples a token
-                if self.cache is not None and s.tokens is not None:
+                s.num_tokens = s.num_cached + s.num_dropped + 1  # the prompt's last position samples a token
+                if self.cache is not None and s.tokens is not None and not s.num_dropped:
                     self.cache.insert(np.asarray(s.tokens)[:s.num_cached], s.block_table)
         self.step_no += 1
 

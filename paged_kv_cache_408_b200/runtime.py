@@ -340,6 +340,8 @@ class KVManager:
         cache names, is replaced by a copy (emitted for ``pa_copy_blocks``).
         Needed before ``pa_compact_kv`` moves tokens inside the sequence,
         and before ``pa_decode_weights`` where sequences share blocks."""
+        if first_pos < 0:
+            raise ValueError(f"first_pos {first_pos} is negative")
         for j in range(first_pos // BLOCK_SIZE, len(seq.block_table)):
             if self._shared(seq.block_table[j]):
                 self._copy_block(seq, j)

@@ -221,3 +221,12 @@ def test_random_histories_keep_lists_pool_and_contents_sound():
                         for x in blocks:
                             sc.alloc.decref(x)
             check_invariants(sc)
+
+
+def test_make_private_refuses_a_negative_position():
+    """(It wrapped around to the sequence's last blocks.)"""
+    sc = Scheduler(BlockAllocator(8), SchedulerConfig(watermark=0.0))
+    b = sc.fork(sc.restore(0, 40, 4), 1, 4)
+    with pytest.raises(ValueError):
+        sc.kv.make_private(b, -1)
+    assert sc.kv.take_copies().size == 0

@@ -140,11 +140,22 @@ int pa_write_kv(const void *k, const void *v, const int64_t *slot_mapping, int64
  * Every element of block src (all kv heads, all 16 slots) is copied to block
  * dst in both caches.  Destinations must be distinct and no destination may
  * also be a source in the same call (pairs run concurrently).
- * Per-head fp8 scales are per cache, not per block: nothing else to copy.
+ * Per-head fp8 scales are per cache, not per block: nothing to copy.  Where
+ * attention weights are kept per block, use pa_copy_blocks_weights.
  * num_pairs == 0 enqueues nothing.
  */
 int pa_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_dst_pairs, int32_t num_pairs,
                    const pa_cache_desc *desc, pa_stream_t stream);
+
+/*
+ * pa_copy_blocks_weights -- pa_copy_blocks, and the same blocks of the
+ * attention weights kept beside the cache (pa_decode_weights): what a copied
+ * block's tokens have gathered so far goes with them.
+ *
+ *   weights       fp32 [num_blocks][num_kv_heads][16], 16-byte aligned.
+ */
+int pa_copy_blocks_weights(void *k_cache, void *v_cache, float *weights, const int32_t *src_dst_pairs,
+                           int32_t num_pairs, const pa_cache_desc *desc, pa_stream_t stream);
 
 /*
  * pa_decode_workspace_size -- bytes of device workspace pa_decode needs for
@@ -386,7 +397,8 @@ int pa_decode_tree(void *out, const void *q, const int32_t *cu_q_lens, const int
  *                 aligned, no initialisation needed; not shared by calls that
  *                 overlap on the GPU.
  * Sequences of one call must hold distinct blocks: a slot that two of them
- * reach (a shared prompt) gets an unspecified one of the two sums.
+ * reach (a shared prompt) gets an unspecified one of the two sums (copy
+ * shared blocks first, pa_copy_blocks_weights).
  */
 int pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq,
                                      const pa_cache_desc *desc, size_t *bytes);
@@ -435,7 +447,7 @@ int pa_select_tokens(int32_t *keep, int32_t *keep_lens, const float *weights, co
  * PA_DEVERR_BAD_LEN and its sequence left as it is.  Positions behind the
  * last kept one keep their old contents.  The blocks moved within must
  * belong to one sequence of the call only (copy shared ones first,
- * pa_copy_blocks).
+ * pa_copy_blocks or, with weights, pa_copy_blocks_weights).
  */
 int pa_compact_kv(void *k_cache, void *v_cache, float *weights, const int32_t *block_tables, const int32_t *keep,
                   const int32_t *keep_lens, const int32_t *start_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
@@ -451,8 +463,8 @@ int pa_get_last_device_error(uint32_t *flags, pa_stream_t stream);
 /* Human-readable name of a pa_status value (static string). */
 const char *pa_status_string(int status);
 
-/* Library version as an integer (major*10000 + minor*100 + patch): 400 =
- * 0.4.0, which adds pa_decode_tree, pa_decode_weights, pa_select_tokens and
+/* Library version as an integer (major*10000 + minor*100 + patch): 401 =
+ * 0.4.1, which adds pa_copy_blocks_weights to 0.4.0; 0.4.0 added pa_decode_tree, pa_decode_weights, pa_select_tokens and
  * pa_compact_kv to 0.3.0; 0.3.0 added chunked prefill over an fp8 cache and the
  * PA_MAX_BLOCKS_PER_SEQ bound to 0.2.0 (pa_decode_cascade,
  * pa_decode_noalloc). */

@@ -87,7 +87,7 @@ int pa::sm_count() {
 
 extern "C" {
 
-int pa_version(void) { return 400; }
+int pa_version(void) { return 401; }
 
 const char *pa_status_string(int status) {
     switch (status) {
@@ -118,17 +118,27 @@ int pa_write_kv(const void *k, const void *v, const int64_t *slot_mapping, int64
     return from_cuda(pa::launch_write_kv(a, static_cast<cudaStream_t>(stream)));
 }
 
-int pa_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_dst_pairs, int32_t num_pairs,
-                   const pa_cache_desc *desc, pa_stream_t stream) {
+static int copy_blocks(void *k_cache, void *v_cache, float *weights, bool with_weights, const int32_t *src_dst_pairs,
+                       int32_t num_pairs, const pa_cache_desc *desc, pa_stream_t stream) {
     int rc = check_desc(desc);
     if (rc != PA_OK) return rc;
     if (num_pairs < 0) return PA_ERR_INVALID_ARG;
     if (num_pairs == 0) return PA_OK;
-    if (!k_cache || !v_cache || !src_dst_pairs) return PA_ERR_INVALID_ARG;
-    if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    if (!k_cache || !v_cache || !src_dst_pairs || (with_weights && !weights)) return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights)) return PA_ERR_INVALID_ARG;
     pa::CopyArgs a{k_cache, v_cache, src_dst_pairs, num_pairs, desc->num_blocks, desc->num_kv_heads,
-                   desc->head_dim, elem_bytes(desc), status_word_ptr()};
+                   desc->head_dim, elem_bytes(desc), status_word_ptr(), weights};
     return from_cuda(pa::launch_copy_blocks(a, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_dst_pairs, int32_t num_pairs,
+                   const pa_cache_desc *desc, pa_stream_t stream) {
+    return copy_blocks(k_cache, v_cache, nullptr, false, src_dst_pairs, num_pairs, desc, stream);
+}
+
+int pa_copy_blocks_weights(void *k_cache, void *v_cache, float *weights, const int32_t *src_dst_pairs,
+                           int32_t num_pairs, const pa_cache_desc *desc, pa_stream_t stream) {
+    return copy_blocks(k_cache, v_cache, weights, true, src_dst_pairs, num_pairs, desc, stream);
 }
 
 int pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t head_dim, int32_t max_blocks_per_seq,

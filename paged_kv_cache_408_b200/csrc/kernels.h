@@ -28,6 +28,7 @@ struct CopyArgs {
     int64_t num_blocks;
     int Hkv, D, elem_bytes;
     unsigned *err;
+    float *weights;  // [num_blocks][Hkv][16], copied too, or nullptr
 };
 
 struct DecodeArgs {

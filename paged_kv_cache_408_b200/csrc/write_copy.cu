@@ -78,10 +78,12 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const uint4 *__restrict__
 }
 
 // One CTA per (pair, cache); the block of all kv heads is one contiguous run
-// of `vecs` 16-byte vectors.
+// of `vecs` 16-byte vectors, in the attention weights (a third row of CTAs,
+// where there are any) of `wvecs`.
 __global__ void __launch_bounds__(256) copy_blocks_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc,
                                                           const int32_t *__restrict__ pairs, int64_t num_blocks,
-                                                          int64_t vecs, unsigned *err) {
+                                                          int64_t vecs, unsigned *err, uint4 *__restrict__ weights,
+                                                          int64_t wvecs) {
     pdl_trigger();
     pdl_wait();
     const int64_t s = pairs[2 * blockIdx.x], d = pairs[2 * blockIdx.x + 1];
@@ -89,7 +91,8 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(uint4 *__restrict__ kc
         if (threadIdx.x == 0) flag_error(err, PA_DEVERR_BAD_PAIR);
         return;
     }
-    uint4 *base = blockIdx.y == 0 ? kc : vc;
+    uint4 *base = blockIdx.y == 0 ? kc : blockIdx.y == 1 ? vc : weights;
+    if (blockIdx.y == 2) vecs = wvecs;
     const uint4 *src = base + s * vecs;
     uint4 *dst = base + d * vecs;
     for (int64_t i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = src[i];
@@ -110,9 +113,9 @@ cudaError_t launch_write_kv(const WriteArgs &a, cudaStream_t st) {
 cudaError_t launch_copy_blocks(const CopyArgs &a, cudaStream_t st) {
     if (a.num_pairs == 0) return cudaSuccess;
     const int64_t vecs = (int64_t)a.Hkv * 16 * a.D * a.elem_bytes / 16;
-    dim3 grid((unsigned)a.num_pairs, 2);
+    dim3 grid((unsigned)a.num_pairs, a.weights ? 3 : 2);
     return launch_pdl(copy_blocks_kernel, grid, dim3(256), 0, st, (uint4 *)a.k_cache, (uint4 *)a.v_cache, a.pairs,
-                      a.num_blocks, vecs, a.err);
+                      a.num_blocks, vecs, a.err, (uint4 *)a.weights, (int64_t)a.Hkv * 4);
 }
 
 }  // namespace pa

@@ -117,12 +117,15 @@ class StepExecutor:
                       written, e.g. to materialise a prompt's cache, but not
                       attended);
     cascade           use cascade decode where the decode rows share blocks;
-    partition_tokens  pa_decode's split (0: balanced).
+    partition_tokens  pa_decode's split (0: balanced);
+    weights           fp32 [num_blocks, Hkv, 16], the attention weights that
+                      the caller keeps beside the cache (ops.decode_weights):
+                      a step's block copies take them along.
     ``reserve(plans)`` sizes the one decode workspace for every step first.
     """
 
     def __init__(self, k_cache, v_cache, Hq, scale=None, k_scale=None, v_scale=None, attend_prefill=True,
-                 cascade=True, partition_tokens=0):
+                 cascade=True, partition_tokens=0, weights=None):
         self.k_cache, self.v_cache = k_cache, v_cache
         self.k_scale, self.v_scale = k_scale, v_scale
         self.Hq = int(Hq)
@@ -131,6 +134,7 @@ class StepExecutor:
         self.attend_prefill = attend_prefill
         self.cascade = cascade
         self.partition = int(partition_tokens)
+        self.weights = weights
         self.ws = None
 
     def workspace_bytes(self, plan: StepPlan) -> int:
@@ -155,7 +159,7 @@ class StepExecutor:
         """The step's copy-on-write copies, then its new K/V."""
         n = 0
         if ds.copies.shape[0]:
-            ops.copy_blocks(self.k_cache, self.v_cache, ds.copies)
+            ops.copy_blocks(self.k_cache, self.v_cache, ds.copies, weights=self.weights)
             n += 1
         if ds.T:
             ops.write_kv(new_k[:ds.T], new_v[:ds.T], ds.slots, self.k_cache, self.v_cache, self.k_scale, self.v_scale)

@@ -28,7 +28,7 @@ EXPORTED = (
     "pa_get_last_device_error", "pa_status_string", "pa_version", "pa_decode_noalloc",
     "pa_decode_cascade_workspace_size", "pa_decode_cascade",
     "pa_decode_tree_workspace_size", "pa_decode_tree", "pa_decode_weights_workspace_size", "pa_decode_weights",
-    "pa_select_tokens", "pa_compact_kv",
+    "pa_select_tokens", "pa_compact_kv", "pa_copy_blocks_weights",
 )
 MAX_TREE_ROWS = 64
 
@@ -58,6 +58,7 @@ def lib():
         p, i32, i64, f32, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
         L.pa_write_kv.argtypes = [p, p, p, i64, p, p, p, p, C.POINTER(CacheDesc), p]
         L.pa_copy_blocks.argtypes = [p, p, p, i32, C.POINTER(CacheDesc), p]
+        L.pa_copy_blocks_weights.argtypes = [p, p, p, p, i32, C.POINTER(CacheDesc), p]
         L.pa_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, C.POINTER(sz)]
         L.pa_decode.argtypes = [p, p, p, p, p, p, i32, i32, i32, f32, p, p, i32, p, sz, C.POINTER(CacheDesc), p]
         L.pa_prefill_chunk.argtypes = [p, p, p, p, p, i32, i32, i32, i32, i32, p, p, f32, p, p,
@@ -173,12 +174,19 @@ def write_kv(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None, s
                                             _ptr(ks), _ptr(vs), C.byref(desc), _stream(stream)))
 
 
-def copy_blocks(k_cache, v_cache, pairs, stream=None):
-    """pa_copy_blocks: pairs int32 [n, 2] = (src, dst)."""
+def copy_blocks(k_cache, v_cache, pairs, stream=None, weights=None):
+    """pa_copy_blocks: pairs int32 [n, 2] = (src, dst); with the attention
+    weights fp32 [num_blocks, Hkv, 16] that decode_weights keeps beside the
+    cache, those of the same blocks too (pa_copy_blocks_weights)."""
     desc = _caches(k_cache, v_cache)
     _need(pairs, "pairs", torch.int32, k_cache.device)
     if pairs.numel() % 2:
         raise ValueError("pairs must be [n, 2]")
+    if weights is not None:
+        w = _token_weights(weights, desc, k_cache.get_device())
+        _check("pa_copy_blocks_weights", lib().pa_copy_blocks_weights(
+            _ptr(k_cache), _ptr(v_cache), w, _ptr(pairs), pairs.numel() // 2, C.byref(desc), _stream(stream)))
+        return
     _check("pa_copy_blocks", lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(pairs), pairs.numel() // 2,
                                                   C.byref(desc), _stream(stream)))
 

@@ -339,7 +339,8 @@ class KVManager:
         every such block that other sequences share, or that the prefix
         cache names, is replaced by a copy (emitted for ``pa_copy_blocks``).
         Needed before ``pa_compact_kv`` moves tokens inside the sequence,
-        and before ``pa_decode_weights`` where sequences share blocks."""
+        and before ``pa_decode_weights`` where sequences share blocks (the
+        copies then take the weights along, ``pa_copy_blocks_weights``)."""
         if first_pos < 0:
             raise ValueError(f"first_pos {first_pos} is negative")
         for j in range(first_pos // BLOCK_SIZE, len(seq.block_table)):

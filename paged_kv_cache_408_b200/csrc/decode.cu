@@ -446,19 +446,15 @@ struct QPrefetch {
     }
 };
 
-// Where a piece's fp32 output and log2-sum-exp go: head h of the group is row
-// base + h * stride of ws_o and ws_lse.
-struct PieceAt {
-    size_t base, stride;
-};
-
+// Row of ws_o and ws_lse for head h of the group of piece `piece` (of the row,
+// behind a cascade's prefix pieces).
 template <class C>
-PA_DEVICE PieceAt piece_at(const DecodeArgs &a, const Item &it, size_t row0, int gw) {
+PA_DEVICE size_t piece_row(const DecodeArgs &a, const Item &it, size_t row0, int h, int piece, int gw) {
     // of the cut segments that a warp meets, only its last one can begin in
     // its share, and only its first one before it: two slots a warp hold
     // every piece, piece p of a segment in warp ws_first + p's
-    if constexpr (C::W) return {((size_t)gw * 2 + (it.piece == 0 ? 1 : 0)) * C::G, 1};
-    return {row0 * a.max_parts + it.piece + a.prefix_pieces, (size_t)a.max_parts};
+    if constexpr (C::W) return ((size_t)gw * 2 + (it.piece == 0 ? 1 : 0)) * C::G + h;
+    return (row0 + h) * a.max_parts + piece;
 }
 
 // Log2-sum-exp of a piece with running maximum m and sum l.  For the attention
@@ -712,11 +708,11 @@ PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &p
             }
             if (lane == 0 && a.ws_np) a.ws_np[(size_t)it.b * Hkv + it.kvh] = 1;
         } else {
-            const PieceAt at = piece_at<C>(a, it, row0, gw);
+            const int piece = it.piece + a.prefix_pieces;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 const float inv = hh ? inv1 : inv0;
-                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + (at.base + (2 * c + hh) * at.stride) * D + r * VB);
+                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + piece_row<C>(a, it, row0, 2 * c + hh, piece, gw) * D + r * VB);
 #pragma unroll
                 for (int i = 0; i < VB / 4; ++i) {
                     float v[4];
@@ -729,8 +725,8 @@ PA_DEVICE void mma_items(const DecodeArgs &a, const Schedule &sc, Producer<C> &p
                 }
             }
             if (r == 0) {
-                a.ws_lse[at.base + 2 * c * at.stride] = piece_lse<C>(m0, l0);
-                a.ws_lse[at.base + (2 * c + 1) * at.stride] = piece_lse<C>(m1, l1);
+                a.ws_lse[piece_row<C>(a, it, row0, 2 * c, piece, gw)] = piece_lse<C>(m0, l0);
+                a.ws_lse[piece_row<C>(a, it, row0, 2 * c + 1, piece, gw)] = piece_lse<C>(m1, l1);
             }
             if (lane == 0 && it.piece == 0) {
                 a.ws_np[(size_t)it.b * Hkv + it.kvh] = it.npieces + a.prefix_pieces;
@@ -1045,12 +1041,12 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                 // ---- split-K: this piece's normalised output and log2-sum-exp;
                 // piece 0 also records how many pieces the merge kernel combines
                 // (in a cascade the pieces follow the shared prefix's pieces)
-                const PieceAt at = piece_at<C>(a, it, row0, gw);
+                const int piece = it.piece + a.prefix_pieces;
                 if (g == 0) {
     #pragma unroll
                     for (int h = 0; h < G; ++h) {
                         const float inv = (l[h] > 0.f) ? vscale / l[h] : 0.f;
-                        float *dst = a.ws_o + (at.base + (h ^ sh) * at.stride) * D;
+                        float *dst = a.ws_o + piece_row<C>(a, it, row0, h ^ sh, piece, gw) * D;
     #pragma unroll
                         for (int c = 0; c < C::NCH; ++c) {
                             float4 *d4 = reinterpret_cast<float4 *>(dst + choff[c] * 8);
@@ -1060,7 +1056,7 @@ __global__ void __launch_bounds__(C::NT, C::MIN_CTAS) decode_kernel(const Decode
                                                 acc2[h][4 * c + 3].x * inv, acc2[h][4 * c + 3].y * inv);
                         }
                         if (sub == 0)  // sub 0 has sh == 0: slot h is head h
-                            a.ws_lse[at.base + h * at.stride] = piece_lse<C>(m[h], l[h]);
+                            a.ws_lse[piece_row<C>(a, it, row0, h, piece, gw)] = piece_lse<C>(m[h], l[h]);
                     }
                 }
                 if (lane == 0 && it.piece == 0) {

@@ -1022,9 +1022,9 @@ __global__ void __launch_bounds__(C::NT, 1)
                 landed = wait_all(&odone[nn & 1], (nn >> 1) & 1);
             }
             const float inv = (l > 0.f ? 1.f / l : l == l ? 0.f : l) * C::OPMUL * (C::FP8 ? a.v_scale[it.kvh] : 1.f);
-            const uint32_t colA = lane_base + C::COL_O + (solo ? g * D : 0), colB = solo ? colA : colA + D;
+            const uint32_t colA = lane_base + C::COL_O + (solo ? g * D : 0);
             const bool dead = l == 0.f;  // sees nothing: zeros
-            const float wA = f0 * inv, wB = f1 * inv;  // (alone: f0 = 1, f1 = 0)
+            const float wA = f0 * inv, wB = f1 * inv;  // (alone: f0 = 1)
             const int c0 = solo ? 0 : g * (D / 2), c1 = solo ? D : c0 + D / 2;
             const bool whole = it.whole();
             const int slot = blockIdx.x * 2 + (it.j0 == 0 ? 1 : 0), srow = slot * 256 + qt * 128;
@@ -1039,13 +1039,21 @@ __global__ void __launch_bounds__(C::NT, 1)
                 float zero = 0.f;  // turns NaN where an output is not finite
 #pragma unroll 1
                 for (int c = c0; c < c1; c += 16) {
-                    float o[16], ob[16];
+                    float o[16];
                     tmem_ld16(colA + c, o);
-                    tmem_ld16(colB + c, ob);
-                    tmem_wait_ld();
+                    if (solo) {  // (no second accumulator: an infinity times a weight of zero would be a NaN)
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= wA;
+                    } else {
+                        float ob[16];
+                        tmem_ld16(colA + D + c, ob);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = fmaf(ob[e], wB, o[e] * wA);
+                    }
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        o[e] = fmaf(ob[e], wB, o[e] * wA);
                         o[e] = dead ? 0.f : o[e];
                         zero = fmaf(o[e], 0.f, zero);
                     }

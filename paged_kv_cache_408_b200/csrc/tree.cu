@@ -768,7 +768,8 @@ __global__ void __launch_bounds__(C::NT, 1)
                             for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
                             int ex = 0;
                             if (amax > 0.f) ex = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xff) - 127), -100), 100);
-                            const float qs = __uint_as_float((uint32_t)(127 + ex) << 23);
+                            // (a negative K scale goes into the query: the softmax counts on a positive one)
+                            const float qs = copysignf(__uint_as_float((uint32_t)(127 + ex) << 23), a.k_scale[it.kvh]);
                             uint32_t h[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -891,15 +892,18 @@ __global__ void __launch_bounds__(C::NT, 1)
             const bool warp_live = (w & 3) * 32 < nrows, row_live = r < nrows;
             const int64_t qrow = it.q0 + qt * C::QPOS + r / G;
             const uint64_t bits = row_live ? a.mask[qrow] : 0;
-            float sl2 = a.scale * kLog2e * C::OPMUL * (C::FP8 ? a.k_scale[it.kvh] : 1.f);
+            float sl2 = a.scale * kLog2e * C::OPMUL * (C::FP8 ? fabsf(a.k_scale[it.kvh]) : 1.f);
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int k = k0; k < steps; k += 2) {
                 const int nn = n + k, kv0 = (it.j0 + (pair ? k >> 1 : k)) * KT;
                 const bool landed = wait_all(&sfull[g], (nn >> 1) & 1);
-                if (C::FP8 && landed && k == k0)
+                if (C::FP8 && landed && k == k0) {
                     sl2 *= __uint_as_float((uint32_t)(127 - qexp[((qc + qt) & 3) * 128 + r]) << 23);
+                    // a K scale of zero: scores (below 2^24) that round to zero, but masked ones stay -inf
+                    if (sl2 == 0.f) sl2 = 0x1p-126f;
+                }
                 const int t = kt + (pair ? k >> 1 : k);
                 const uint32_t bad = badmask[t % C::NBAD];
                 if constexpr (!C::FP8) {  // V rows past the end or of bad blocks: zero them before they meet P

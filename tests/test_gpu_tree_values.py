@@ -7,7 +7,7 @@ import torch
 
 import cache_ops_util as U
 from paged_kv_cache_408_b200 import ops
-from test_gpu_cache_ops import make_tree, run_tree
+from test_gpu_cache_ops import check_tree, make_tree, run_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,14 @@ def test_infinite_value_in_the_prefix(cuda_device, prefix, T, G, value):
     ref, tol = U.tree64(c, q, cu, pre, mask, scale, 2.0 ** -8)
     rest = torch.arange(64) != 5
     assert bool(((out - ref).abs()[:, :, rest] <= tol[:, :, rest]).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [2, 8])
+def test_any_finite_head_scale(cuda_device, G, D):
+    """K scales that are zero (every visible key weighs the same) or negative,
+    V scales likewise, in tiles with and without masked keys."""
+    c, q, cu, pre, mask, scale = make_tree(92, [0, 100, 1000, 31], [5, 40, 3, 1], 4, G, D, fp8=True)
+    c.k_scale = torch.tensor([0.0, -0.013, 0.011, -0.0])
+    c.v_scale = torch.tensor([0.012, 0.014, 0.0, -0.01])
+    check_tree(c, q, cu, pre, mask, scale)

@@ -16,7 +16,8 @@
 // tile), cut into equal contiguous shares, one per SM.  Of the segments a
 // CTA meets only its first can have begun before its share and only its last
 // can go on behind it, so two slots a CTA hold every partial result, whatever
-// the batch; the merge kernel joins them by log-sum-exp.
+// the batch; the merge kernel joins them by log-sum-exp (tree_split.h, which
+// the tests compile for the host).
 //
 // Within a CTA the work is a line of steps, each the scores, softmax and P.V
 // of one row tile and one key tile; steps alternate between two streams, each
@@ -60,14 +61,13 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tree_split.h"
 
 namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the running maximum may lag behind
-// line units of a key tile, in a segment of one and of two row tiles
-constexpr int kOne = 2, kPair = 3;
 constexpr int kMaxCtas = 160;              // partial-result slots: two a CTA
 constexpr int kEpiBar = 1;                 // named barrier of the softmax warps
 constexpr unsigned kFull = 0xffffffffu;
@@ -76,7 +76,7 @@ template <int D_, int G_, bool FP8_>
 struct TCfg {
     static constexpr int D = D_, G = G_;
     static constexpr bool FP8 = FP8_;
-    static constexpr int M = 128, KT = 128, BPT = KT / 16;
+    static constexpr int M = kTreeRows, KT = kTreeKeys, BPT = KT / 16;
     static constexpr int QPOS = M / G;             // drafts of a row tile
     static constexpr int NATOM = D / 64;           // 128-byte column atoms along D
     static constexpr int ATOM = 128 * 128;         // bytes of one atom column of a 128-row tile
@@ -114,7 +114,7 @@ struct TCfg {
     // line units of a segment itself (its query tile, first tile and epilogue):
     // 64 x 100 tokens take 3.0 us a segment of one tile against 1.45 us a tile
     // (bf16), 8 against 2 us (E4M3)
-    static constexpr int SEG = FP8 ? 7 : 5;
+    static constexpr int SEG = FP8 ? kSegE4m3 : kSegBf16;
     // the next item's first K tile before this one's last V tile, or behind
     // it: widening K takes as long as a softmax, so E4M3 wants it early (64 x
     // 1000 tokens, 16 drafts: 102 against 108 us); a bf16 tile is only a copy
@@ -136,108 +136,6 @@ struct TreeWs {
     float *o;    // [2 kMaxCtas][256][D] normalised partial outputs
     float *lse;  // [2 kMaxCtas][256] log2-sum-exp
     int4 *desc;  // [kMaxCtas]: (first q row, rows, kv head, pieces) of the cut segment that begins in CTA g; pieces 0: none
-};
-
-// A sequence of the batch: its metadata as loaded, and checked.
-struct Raw {
-    int q0, q1, P;
-};
-struct Seq {
-    int q0, T, P;          // first row, drafts (0 if its metadata is bad), prefix
-    int nt, npair, none;   // key tiles; segments of two and of one row tile per kv head
-    PA_DEVICE int units_head(int seg) const { return npair * (seg + nt * kPair) + none * (seg + nt * kOne); }
-};
-
-PA_DEVICE Raw load_raw(const TreeArgs &a, int b) {
-    b = min(b, a.B - 1);
-    return {a.cu_q[b], a.cu_q[b + 1], a.prefix_lens[b]};
-}
-
-template <class C>
-PA_DEVICE Seq make_seq(const TreeArgs &a, const Raw &x, bool flag) {
-    Seq s;
-    const int64_t T = (int64_t)x.q1 - x.q0;
-    const bool bad = x.q0 < 0 || T < 0 || T > a.max_q_len || x.q1 > a.total_q || x.P < 0 ||
-                     x.P + T > (int64_t)a.max_blocks * 16;
-    if (bad && flag) flag_error(a.err, PA_DEVERR_BAD_LEN);
-    s.q0 = x.q0;
-    s.T = bad ? 0 : (int)T;
-    s.P = bad ? 0 : x.P;
-    const int nmt = (s.T + C::QPOS - 1) / C::QPOS;
-    s.npair = nmt >> 1;
-    s.none = nmt & 1;
-    s.nt = (s.P + s.T + C::KT - 1) / C::KT;
-    return s;
-}
-
-// Key tiles [j0, j1) of one segment.
-struct Item {
-    int b, kvh, q0, T, P, L;   // q0: first row of the segment; T: drafts of the sequence
-    int r0, rt;                // first draft of the segment; its row tiles, 1 or 2
-    int j0, j1, nt;            // nt: key tiles of the segment
-    int tile0;                 // line position of its first tile
-    PA_DEVICE int steps() const { return (j1 - j0) * rt; }
-    PA_DEVICE bool whole() const { return j0 == 0 && j1 == nt; }
-};
-
-// Walks a CTA's share of the line.
-template <class C>
-struct Walk {
-    int pos, end, base;  // base: line position of sequence b
-    int S, b;
-    Seq s;
-    Raw nxt;                 // sequence b + 1, loaded ahead
-
-    PA_DEVICE void start(const TreeArgs &a, int pos_, int end_, int S_, int b0, int base0) {
-        pos = pos_, end = end_, S = S_, b = b0, base = base0;
-        if (pos < end) {
-            s = make_seq<C>(a, load_raw(a, b), false);
-            nxt = load_raw(a, b + 1);
-        }
-    }
-    PA_DEVICE bool next(const TreeArgs &a, Item &it) {
-#pragma unroll 1
-        while (pos < end) {
-            const int head = s.units_head(C::SEG), off = pos - base;
-            if (off >= head * a.Hkv) {
-                base += head * a.Hkv;
-                s = make_seq<C>(a, nxt, false);
-                nxt = load_raw(a, ++b + 1);
-                continue;
-            }
-            it.kvh = off / head;
-            int r = off - it.kvh * head;           // unit within the kv head's segments, then within the segment
-            const int Up = C::SEG + s.nt * kPair;
-            int seg = r / Up;
-            it.rt = seg < s.npair ? 2 : 1;
-            seg = min(seg, s.npair);
-            r -= seg * Up;
-            const int wt = it.rt == 2 ? kPair : kOne, U = C::SEG + s.nt * wt;
-            const int stop = min(U, end - pos + r);
-            // the tiles whose first unit lies in the share
-            it.j0 = max(0, r - C::SEG + wt - 1) / wt;
-            it.j1 = max(0, stop - C::SEG + wt - 1) / wt;
-            const int seg0 = pos - r;
-            pos = seg0 + stop;
-            if (it.j1 <= it.j0) continue;
-            it.b = b;
-            it.r0 = 2 * seg * C::QPOS;
-            it.q0 = s.q0 + it.r0;
-            it.T = s.T;
-            it.P = s.P;
-            it.L = s.P + s.T;
-            it.nt = s.nt;
-            it.tile0 = seg0 + C::SEG;
-            return true;
-        }
-        return false;
-    }
-    // pieces of a segment: one for every share from the one that holds its
-    // first tile's first unit to the one that holds its last tile's
-    PA_DEVICE int pieces(const Item &it) const {
-        const int last = it.tile0 + (it.nt - 1) * (it.rt == 2 ? kPair : kOne);
-        return last / S - it.tile0 / S + 1;
-    }
 };
 
 // One cache row's elements of a lane, widened to fp32.
@@ -469,8 +367,11 @@ __global__ void __launch_bounds__(C::NT, 1)
         const int per = (a.B + C::NT - 1) / C::NT, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
         int mine = 0;  // (the whole line has less than 2^31 units: checked on the host)
 #pragma unroll 1
-        for (int b = b0; b < b1; ++b)
-            mine += make_seq<C>(a, load_raw(a, b), blockIdx.x == 0).units_head(C::SEG) * a.Hkv;
+        for (int b = b0; b < b1; ++b) {
+            const Seq q = make_seq<C>(a, load_raw(a, b));
+            if (q.bad && blockIdx.x == 0) flag_error(a.err, PA_DEVERR_BAD_LEN);
+            mine += q.units_head(C::SEG) * a.Hkv;
+        }
         int x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -485,13 +386,13 @@ __global__ void __launch_bounds__(C::NT, 1)
             if (i < w) before += scan[i];
             total += scan[i];
         }
-        const int S = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kPair);  // at least a tile's units
+        const int S = tree_share(total, gridDim.x);
         const int64_t pos = (int64_t)blockIdx.x * S;  // (may lie past the line)
         if (pos >= before && pos < before + mine) {  // one thread at most
             int at = before;
             int b = b0;
             for (;; ++b) {
-                const int u = make_seq<C>(a, load_raw(a, b), false).units_head(C::SEG) * a.Hkv;
+                const int u = make_seq<C>(a, load_raw(a, b)).units_head(C::SEG) * a.Hkv;
                 if (pos < at + u) break;
                 at += u;
             }
@@ -885,7 +786,7 @@ __global__ void __launch_bounds__(C::NT, 1)
                 n += steps;
                 kt += it.j1 - it.j0;
                 qc += it.rt;
-                if (!it.whole() && it.j0 == 0) desc = make_desc(it);
+                if (it.begins_cut()) desc = make_desc(it);
                 continue;
             }
             const int nrows = min(C::QPOS, it.T - it.r0 - qt * C::QPOS) * G;
@@ -1031,7 +932,7 @@ __global__ void __launch_bounds__(C::NT, 1)
             const float wA = f0 * inv, wB = f1 * inv;  // (alone: f0 = 1)
             const int c0 = solo ? 0 : g * (D / 2), c1 = solo ? D : c0 + D / 2;
             const bool whole = it.whole();
-            const int slot = blockIdx.x * 2 + (it.j0 == 0 ? 1 : 0), srow = slot * 256 + qt * 128;
+            const int srow = it.slot(blockIdx.x) * 256 + qt * 128;
             auto out_row = [&](int rr) {
                 return static_cast<__nv_bfloat16 *>(a.out) +
                        ((it.q0 + qt * C::QPOS + rr / G) * (int64_t)a.Hq + it.kvh * G + rr % G) * D;
@@ -1106,7 +1007,7 @@ __global__ void __launch_bounds__(C::NT, 1)
             n += steps;
             kt += it.j1 - it.j0;
             qc += it.rt;
-            if (!whole && it.j0 == 0) desc = make_desc(it);
+            if (it.begins_cut()) desc = make_desc(it);
         }
         if (tid == 0) ws.desc[blockIdx.x] = desc;
     }
@@ -1146,7 +1047,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a, const
     const int4 d = __ldcg(ws.desc + g);
 #pragma unroll 1
     for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < 256; r += gridDim.y * 4) {
-        auto at = [&](int p) { return (size_t)(2 * (g + p) + (p == 0 ? 1 : 0)) * 256 + r; };
+        auto at = [&](int p) { return (size_t)tree_piece_slot(g, p) * 256 + r; };
         float lse[kMergeAhead], o[kMergeAhead][E];
 #pragma unroll
         for (int p = 0; p < kMergeAhead; ++p) {

@@ -95,7 +95,8 @@ typedef enum pa_dtype {
                                    * tree: a row range or draft count out of bounds; compact: a list past its bounds */
 #define PA_DEVERR_BAD_PAIR 0x8u   /* a copy pair outside [0, num_blocks); compact: a list that does not ascend */
 #define PA_DEVERR_TIMEOUT 0x10u   /* a bounded wait for an async copy or MMA gave up (results invalid) */
-#define PA_DEVERR_LAYOUT 0x20u    /* prefill: the CTA's shared memory did not start on a 1 KB boundary (no output written) */
+#define PA_DEVERR_LAYOUT 0x20u    /* prefill, tree: a CTA's shared memory did not start on a 1 KB boundary (its output
+                                   * is not written) */
 
 /* An opaque stream handle: pass a cudaStream_t. */
 typedef void *pa_stream_t;

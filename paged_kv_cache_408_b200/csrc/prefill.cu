@@ -56,14 +56,13 @@
 //    discrete simulation over random schedules.
 //  * Key rows past the sequence end in the last V tile are zeroed in shared
 //    memory before P.V, so stale cache contents can never reach the output.
-#include <cudaTypedefs.h>
-
 #include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "fastexp.cuh"
 #include "tc.cuh"
+#include "tma_map.h"
 
 namespace pa {
 namespace {
@@ -912,19 +911,6 @@ __global__ void __launch_bounds__(C::NT, 1)
 }
 
 // ---- host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // The cache seen as a 2-D bf16 tensor [num_blocks*Hkv*16 rows][D]; a box is
 // 16 rows (one block of one kv head) x 64 columns, 128-byte swizzled.
 bool cache_map(CUtensorMap *map, const void *base, int64_t rows, int D) {

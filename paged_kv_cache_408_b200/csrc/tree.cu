@@ -53,14 +53,13 @@
 // scores against the maximum so far, repeated where it moved (P of a
 // whole tile in registers: spills with an E4M3 cache); registers moved between warpgroups (the calls of the rare
 // path cannot be compiled so).
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tma_map.h"
 #include "tree_split.h"
 
 namespace pa {
@@ -1096,19 +1095,6 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a, const
 }
 
 // ---- host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // A tensor of `rank` dims (innermost first) with byte strides for all but the
 // first, copied in boxes of `box`.
 bool tiled_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,

@@ -623,6 +623,8 @@ __global__ void __launch_bounds__(C::NT, 1)
         int qc = 0;
 #pragma unroll 1
         while (ok && (C::FP8 || w == C::W_QUERY) && walk.next(a, it)) {
+            // E4M3: a negative K scale goes into the query: the softmax counts on a positive one
+            const uint32_t sign = C::FP8 ? __float_as_uint(a.k_scale[it.kvh]) & 0x80000000u : 0;
 #pragma unroll 1
             for (int qt = 0; qt < it.rt && ok; ++qt, ++qc) {
                 const int sl = qc & 1;
@@ -668,8 +670,7 @@ __global__ void __launch_bounds__(C::NT, 1)
                             for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
                             int ex = 0;
                             if (amax > 0.f) ex = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xff) - 127), -100), 100);
-                            // (a negative K scale goes into the query: the softmax counts on a positive one)
-                            const float qs = copysignf(__uint_as_float((uint32_t)(127 + ex) << 23), a.k_scale[it.kvh]);
+                            const float qs = __uint_as_float(sign | (uint32_t)(127 + ex) << 23);
                             uint32_t h[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {

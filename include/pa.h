@@ -396,7 +396,10 @@ int pa_decode_tree(void *out, const void *q, const int32_t *cu_q_lens, const int
  *                 pa_decode (balanced split).
  *   workspace     at least pa_decode_weights_workspace_size() bytes, 256-byte
  *                 aligned, no initialisation needed; not shared by calls that
- *                 overlap on the GPU.
+ *                 overlap on the GPU.  It holds every score: 4 bytes for each
+ *                 sequence, query head and position of the tables' width,
+ *                 however few tokens are cached (256 sequences, 64 heads and
+ *                 2,048 blocks: 2.1 GB).
  * Sequences of one call must hold distinct blocks: a slot that two of them
  * reach (a shared prompt) gets an unspecified one of the two sums (copy
  * shared blocks first, pa_copy_blocks_weights).
@@ -424,6 +427,8 @@ int pa_decode_weights(void *out, float *weights, const void *q, const void *k_ca
  *                 budget keeps every token.
  * budget >= 1, num_sink + num_recent <= budget, num_seqs in [0, 2048],
  * num_kv_heads <= 128.  Blocks of a bad table entry count as weight -inf.
+ * The work is planned for the tables' width (lengths are read on the device):
+ * tables much wider than the sequences cost time.
  * Only num_blocks and num_kv_heads of `desc` matter.
  */
 int pa_select_tokens(int32_t *keep, int32_t *keep_lens, const float *weights, const int32_t *block_tables,

@@ -163,7 +163,7 @@ constexpr int kMaxDecodeSeqs = 2048;
 constexpr int kMinShareBlocks = 16;  // balanced split: smallest per-warp share, in cost units
 constexpr int kMaxDecodeKvHeads = 128;
 constexpr int kMinScoreShare = 2;     // the same for launch_decode_scores, whose pieces take no room by their count
-constexpr int kMaxScoreWarps = 1920;  // launch_decode_scores: most warps (12 an SM, 148 SMs)
+constexpr int kMaxScoreWarps = 1920;  // launch_decode_scores: most warps (12 an SM on up to 160 SMs)
 // Widest block table any entry point accepts (PA_MAX_BLOCKS_PER_SEQ): token
 // positions (16 * max_blocks) and piece counts stay far inside int32.
 constexpr int kMaxBlocksPerSeq = PA_MAX_BLOCKS_PER_SEQ;

@@ -28,6 +28,10 @@
 //   * Bound: the chain of passes (latency), not bytes: 4 B a token would take
 //     0.5 us for 64 sequences of U[1,2048] tokens and 8 heads (9.8 us in a
 //     graph) and 1.6 us for the long rows above (28 us).
+//   * The plan goes by the tables' width, since the host does not know the
+//     lengths: those 64 sequences take 9.1 us in tables of 128 blocks, 21 us in
+//     tables of 512 (two CTAs a row) and 152 us in tables of 8,192 (eight, most
+//     of them without a token).
 //     Counting the many exact zeros in registers instead of by atomics
 //     changed nothing.
 //
@@ -46,11 +50,15 @@
 //     memory, so that the groups' reads wait for nothing.
 //   * 16-byte vectors; a thread moves the same vector of K and V.
 //   * Entries that are in place already are skipped.
-//   * Bound: HBM, each moved row read and written once: 34 us for 64 x
-//     U[1,2048] tokens cut to 512 (204 MB, 6.0 TB/s), 99 us for 8 x 32768
-//     E4M3 tokens halved (549 MB, 5.5 TB/s).  With the list read inside the
-//     group loop they took 72 and 227 us; two CTAs an SM that request the
-//     next group before the barrier 37 and 118.
+//   * Each moved row is read and written once.  Calls back to back, so that
+//     what a kernel leaves in L2 to be written counts: 44 us for 64 x
+//     U[1,2048] tokens cut to 512 (204 MB, 4.7 TB/s; one CTA a row, 384 of the
+//     512 have work, and the SMs that got four of them end last), 105 us for
+//     8 x 32768 E4M3 tokens halved (549 MB, 5.2 TB/s: HBM).  The kernels alone
+//     take 35 and 100 us, in which a part of their writes (half of the first
+//     one's) has not reached HBM; with the list read inside the group loop 72
+//     and 227 us, with two CTAs an SM that request the next group before the
+//     barrier 37 and 118.
 #include <algorithm>
 #include <mutex>
 

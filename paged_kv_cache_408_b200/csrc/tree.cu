@@ -33,17 +33,24 @@
 // Warps whose 32 rows are all past the drafts skip the arithmetic.
 // An E4M3 cache: the codes land in a staging ring and four warps widen them
 // to f16 operand tiles; two more scale the query rows by a power of two into
-// f16's range.  f16 and not bf16 because every code is an f16 value and P
-// keeps three more bits.
+// f16's range (which rounds components below 2^-28 of their row's largest).
+// f16 and not bf16 because every code is an f16 value and P keeps three more
+// bits.
+// P is rounded for its product alone, to the cache's own type: both operands
+// of an MMA have one type, and V in bf16 has 8 bits as well.  That is up to
+// 2^-8 of a weight (f16: 2^-11); the row's sum takes the weights unrounded.
+// Against 64 bits, relative to the outputs' size: 2.1e-3 to 2.3e-3, of which
+// the bf16 output alone is 1.7e-3; E4M3: 1.7e-3.
 //
 // Bound (kernel alone, 8 kv heads, head_dim 128):
 //   16 x 32701 tokens, 32 drafts (128 rows a kv head): 334 us, 2.15 GB,
 //     6.4 TB/s, tensor pipe 45% -- HBM; called back to back for a second the
-//     1 kW power cap lowers the clock to 1.3 GHz and a call takes 410 us.
-//   64 x U[1,2048], 16 drafts: 66 us, 277 MB -- HBM and the segments: one of
-//     a single key tile takes 3.0 us against 1.45 us for a tile in a row
-//     (query tile, softmax, P.V and epilogue follow one another once).
-//   E4M3, 32 x U[1,8192], U[1,64] drafts of 64 heads: 269 us -- latency: no
+//     1 kW power cap lowers the clock to 1.3 GHz and a call takes 390-415 us.
+//   64 x U[1,2048], 16 drafts: 66 us, 290 MB, 4.4 TB/s -- the segments, 3.5 a
+//     CTA: one of a single key tile takes 3.0 us against 1.45 us for a tile in
+//     a row (query tile, softmax, P.V and epilogue follow one another once),
+//     and its rows fill half of a row tile.
+//   E4M3, 32 x U[1,8192], U[1,64] drafts of 64 heads: 260 us -- latency: no
 //     pipe is above 45% busy; a step's scores wait for the P.V that frees
 //     their columns, and 16 warps leave 128 registers a thread.
 // Measured and dropped: 64-key steps with two score buffers a stream (every
